@@ -719,7 +719,8 @@ EncodeTiledFn get_encode() {
   return fn;
 }
 
-// 3-D map over a token-major [rows, H, d] tensor: dims (d, H, rows), box (box_d, 1, box_rows).
+}  // namespace
+
 bool make_map(CUtensorMap* m, const void* ptr, bool fp8, int d, int H, long long rows, int box_d, int box_rows) {
   EncodeTiledFn enc = get_encode();
   if (enc == nullptr) return false;
@@ -733,6 +734,8 @@ bool make_map(CUtensorMap* m, const void* ptr, bool fp8, int d, int H, long long
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+namespace {
 
 template <int D, int BN, bool FP8, bool PAGED, bool DENSE, int PART, bool SHKV, bool LSEX, bool SNAKE>
 cudaError_t run_k(const BsaParams& prm, cudaStream_t st) {

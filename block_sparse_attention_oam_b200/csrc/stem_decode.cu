@@ -1,0 +1,783 @@
+// Attention of the newest tokens over a paged K/V cache (decoding), sm_100a.
+//
+// For every row (sequence b, new token t, q-head h), over its keys j:
+//   o = sum_j p_j v_j / sum_j p_j,   p_j = exp2(s_j - m),   s_j = sigma log2(e) q.k_j,
+// kept as (m, l = sum p, O = sum p v) so that shares of the keys computed apart can be
+// joined: with M = max m_i,  l = sum_i 2^(m_i - M) l_i,  O = sum_i 2^(m_i - M) O_i.
+//
+// What bounds it: a step reads every cached K and V row once and does 4 d flops per row
+// and key with it, G * q_len (4 to 16) flops a byte, far under the tensor cores' 250; so
+// it is the cache's bytes over the memory bandwidth.  The kernel is built to keep TMA
+// loads in flight and to give every SM the same number of bytes:
+//   - The work is a line of 64-token tiles (one K page and one V page of one kv-head),
+//     sequence after sequence; CTA c of a grid of two per SM takes an equal share, the
+//     lengths being read on the device.  A unit (the up to 16 rows that read one kv-head
+//     of one sequence) whose tiles fall to several CTAs leaves one partial each, joined by
+//     decode_finish; a unit inside one CTA is written out directly.
+//   - One producer warp loads tiles into a ring of 96 KB per CTA (192 KB in flight per SM).
+//   - Four consumer warps each take 16 tokens of every tile with running statistics of
+//     their own, so that nothing in the loop waits for another warp; they are joined in
+//     shared memory at a unit's end.  m16n8k16 matrix instructions with the rows as M: a
+//     128-row tcgen05 tile would hold 4 rows here, and its softmax would still be
+//     one thread per row.
+//   - FP8: K and V codes are widened to f16 in registers, which is exact, and P is rounded
+//     to f16 (2^-11), not to e4m3.  BF16: P is rounded to bf16 (2^-8 at most 2^-9
+//     relative), as V is; the sums l are those of the unrounded p.
+// Waits are bounded; on expiry the CTA raises its abort flag, records STEM_ERR_TIMEOUT and
+// runs through the rest of its units without computing.
+#include <string.h>
+
+#include <type_traits>
+
+#include "stem_internal.cuh"
+
+namespace stem {
+namespace {
+
+constexpr int kThreads = 160;       // four consumer warps, one producer warp
+constexpr int kFinishThreads = 256;
+constexpr int kTile = STEM_PAGE_SIZE;
+static_assert(kTile == 64, "a tile is one page: four warps of 16 tokens");
+
+template <int D, bool FP8>
+struct Cfg {
+  static constexpr int ES = FP8 ? 1 : 2;
+  static constexpr int CH = 128 / ES;               // elements of a 128-byte swizzle row
+  static constexpr int DCH = D * ES / 128;          // such rows per token
+  static constexpr int CHUNK = kTile * 128;         // one box: 64 tokens of 128 bytes
+  static constexpr int TILE = kTile * D * ES;
+  static constexpr int STAGE = 2 * TILE;            // K and V
+  static constexpr int NST = 96 * 1024 / STAGE;
+  static constexpr int MERGE = 4 * 8 * 64 * 4;      // four warps x 8 rows x 64 columns
+  static constexpr int OFF_MERGE = NST * STAGE;
+  static constexpr int OFF_ML = OFF_MERGE + MERGE;  // float2 [4][16]
+  static constexpr int OFF_BAR = OFF_ML + 512;
+  static constexpr int SMEM = OFF_BAR + 512 + 1024;  // 1024: alignment
+  static_assert(DCH >= 1 && NST >= 3 && NST <= 16, "ring");
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(MERGE >= (STEM_MAX_DECODE_SEQS + 1) * 4, "the plan's table is built in the merge buffer");
+};
+
+struct DecodeParams {
+  CUtensorMap tk, tv;        // [slots * 64, Hkv, d]: box (CH, 1, 64)
+  DecodeArgs a;
+  int rt, prt;               // 16-row tiles of a unit's rows: own, prefix (0: no prefix)
+  int prefix_pages, prefix_tiles;
+  int ctas;
+};
+
+__device__ __forceinline__ int clamp_len(const DecodeArgs& a, int b) {
+  return min(max(__ldg(a.kv_lens + b), 0), a.max_kv_len);
+}
+__device__ __forceinline__ int pages_of(int len) { return (len + kTile - 1) / kTile; }
+
+// One CTA's share of one unit.
+struct Seg {
+  bool own;
+  int b, kvh, rtile, unit;
+  int p0, p1, pages, len;
+};
+
+// Walks the units of the tiles [t, end) in line order.
+struct Walk {
+  int t, end, b, base, len;
+  __device__ __forceinline__ bool next(const DecodeParams& p, Seg* s) {
+    if (t >= end) return false;
+    if (t < p.prefix_tiles) {
+      const int u = t / p.prefix_pages;
+      s->own = false;
+      s->unit = u;
+      s->kvh = u / p.prt;
+      s->rtile = u % p.prt;
+      s->b = 0;
+      s->pages = p.prefix_pages;
+      s->len = p.a.prefix_len;
+      s->p0 = t - u * p.prefix_pages;
+    } else {
+      const int per_page = p.a.Hkv * p.rt;
+      int pages = pages_of(len);
+      while (t >= base + pages * per_page) {
+        base += pages * per_page;
+        len = clamp_len(p.a, ++b);
+        pages = pages_of(len);
+      }
+      const int u = (t - base) / pages;
+      s->own = true;
+      s->unit = p.a.Hkv * (p.prt + b * p.rt) + u;
+      s->kvh = u / p.rt;
+      s->rtile = u % p.rt;
+      s->b = b;
+      s->pages = pages;
+      s->len = len;
+      s->p0 = t - base - u * pages;
+    }
+    s->p1 = min(s->pages, s->p0 + (end - t));
+    t += s->p1 - s->p0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// 16-bit masks of a fragment register that holds tokens j and j + 1: the halves whose
+// token is at or behind `limit` become zero (masked V rows may hold NaN).
+__device__ __forceinline__ uint32_t keep_below(int j, int limit) {
+  return (j < limit ? 0xFFFFu : 0u) | (j + 1 < limit ? 0xFFFF0000u : 0u);
+}
+
+template <int D, bool FP8, bool SCORES>
+__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_constant__ DecodeParams p) {
+  using C = Cfg<D, FP8>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sring = smem_u32(smem);
+  float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE);
+  float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+  const uint32_t bars = smem_u32(smem + C::OFF_BAR);
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto empty = [&](int s) { return bars + 128 + 8 * s; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 256);
+  int* plan = reinterpret_cast<int*>(smem + C::OFF_BAR + 260);        // start sequence, its first tile, total
+  int* warp_sums = reinterpret_cast<int*>(smem + C::OFF_BAR + 288);   // [5]
+  const DecodeArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const unsigned all = 0xffffffffu;
+
+  pdl_trigger();
+  if (tid == 0) {
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 4);
+    }
+    *abort_flag = 0;
+    plan[0] = 0;
+    plan[1] = p.prefix_tiles;
+    mbar_fence_init();
+  }
+  // first tile of every sequence (exclusive sums of the unit tiles), 160 sequences at a time
+  int* cum = reinterpret_cast<int*>(merge);
+  int run = p.prefix_tiles;
+  const int per_page = a.Hkv * p.rt;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + tid;
+    int x = 0;
+    if (b < a.B) {
+      const int raw = __ldg(a.kv_lens + b);
+      if (blockIdx.x == 0 && (raw < 0 || raw > a.max_kv_len)) atomicOr(a.status, kStatusBounds);
+      x = pages_of(min(max(raw, 0), a.max_kv_len)) * per_page;
+    }
+    int inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(all, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    int before = run, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += warp_sums[w];
+      sum += warp_sums[w];
+    }
+    if (b < a.B) cum[b] = before + inc - x;
+    run += sum;
+  }
+  if (tid == 0) cum[a.B] = run;
+  __syncthreads();
+  const int per = (run + p.ctas - 1) / p.ctas;
+  const int t0 = min(run, static_cast<int>(blockIdx.x) * per), t1 = min(run, t0 + per);
+  for (int b = tid; b < a.B; b += kThreads) {
+    if (cum[b] <= t0 && t0 < cum[b + 1]) {
+      plan[0] = b;
+      plan[1] = cum[b];
+    }
+  }
+  if (blockIdx.x == 0)
+    for (int b = tid; b <= a.B; b += kThreads) a.cum[b] = cum[b];
+  __syncthreads();
+  Walk walk{t0, t1, plan[0], plan[1], clamp_len(a, plan[0])};
+  Seg sg;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_map(&p.tk);
+      tma_prefetch_map(&p.tv);
+    }
+    uint32_t it = 0;
+    bool alive = true;
+    while (alive && walk.next(p, &sg)) {
+      const int32_t* table = sg.own ? a.table + static_cast<long long>(sg.b) * a.max_pages : a.prefix_table;
+      for (int q0 = sg.p0; q0 < sg.p1 && alive; q0 += 32) {
+        int slot = 0;
+        if (q0 + lane < sg.p1) {
+          slot = __ldg(table + q0 + lane);
+          if (slot < 0 || slot >= a.num_slots) {
+            atomicOr(a.status, kStatusBounds);
+            slot = 0;
+          }
+        }
+        const int cnt = min(32, sg.p1 - q0);
+        for (int q = 0; q < cnt; ++q, ++it) {
+          const int row = __shfl_sync(all, slot, q) * kTile;
+          const int st = it % C::NST;
+          const bool ok = mbar_wait(empty(st), ((it / C::NST) & 1) ^ 1, abort_flag, a.status);
+          if (!__all_sync(all, ok)) {
+            alive = false;
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full(st), C::STAGE);
+            const uint32_t dst = sring + st * C::STAGE;
+#pragma unroll
+            for (int c = 0; c < C::DCH; ++c) {
+              tma_load_3d(dst + c * C::CHUNK, &p.tk, full(st), c * C::CH, sg.kvh, row);
+              tma_load_3d(dst + C::TILE + c * C::CHUNK, &p.tv, full(st), c * C::CH, sg.kvh, row);
+            }
+          }
+        }
+      }
+    }
+    if (!alive)  // let the copies already issued land before the CTA can exit
+      for (uint32_t q = it > C::NST ? it - C::NST : 0; q < it; ++q)
+        for (int spin = 0; spin < 1000000 && !mbar_try_wait(full(q % C::NST), (q / C::NST) & 1); ++spin) {}
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int r0 = lane / 4, qd = lane % 4, mi = lane / 8;
+  const int G = a.G;
+  // this lane's row of the ldmatrix groups of a warp's 16 tokens, and its swizzled chunks
+  const uint32_t k_row = static_cast<uint32_t>(warp * 16 + (FP8 ? (mi & 1) : (mi >> 1)) * 8 + (lane & 7)) * 128;
+  const uint32_t v_row = static_cast<uint32_t>(warp * 16 + (mi & 1) * 8 + (lane & 7)) * 128;
+  const int k_sub = FP8 ? mi >> 1 : mi & 1, v_sub = mi >> 1;
+  const int sw = lane & 7;
+  uint32_t it = 0;
+  while (walk.next(p, &sg)) {
+    const int rows_all = sg.own ? a.n * G : a.B * a.n * G;
+    const int first = sg.rtile * kDecodeRows;
+    const int nrows = min(kDecodeRows, rows_all - first);
+    const int row_base = (sg.own ? sg.b * a.n * G : 0) + first;
+    // keys that the unit's first and last row, and this thread's two rows, see
+    auto limit_of = [&](int r) {
+      if (!sg.own) return sg.len;
+      return max(0, sg.len - a.n + (first + r) / G + 1);
+    };
+    const int lim_lo = limit_of(0), lim_hi = limit_of(nrows - 1);
+    const int lim0 = limit_of(min(r0, nrows - 1)), lim1 = limit_of(min(r0 + 8, nrows - 1));
+    // Q fragments
+    uint32_t qf[D / 16][4];
+    {
+      const unsigned char* qb = static_cast<const unsigned char*>(a.q);
+      const int g0 = row_base + r0, g1 = row_base + r0 + 8;
+      const unsigned char* q0 =
+          qb + (static_cast<long long>(g0 / G) * a.Hq + sg.kvh * G + g0 % G) * D * C::ES + qd * 4;
+      const unsigned char* q1 =
+          qb + (static_cast<long long>(g1 / G) * a.Hq + sg.kvh * G + g1 % G) * D * C::ES + qd * 4;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        if (FP8) {
+          const uint32_t x = r0 < nrows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 16)) : 0u;
+          const uint32_t y = r0 + 8 < nrows ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 16)) : 0u;
+          qf[k][0] = e4m3x2_to_h2(x & 0xFFFFu);
+          qf[k][2] = e4m3x2_to_h2(x >> 16);
+          qf[k][1] = e4m3x2_to_h2(y & 0xFFFFu);
+          qf[k][3] = e4m3x2_to_h2(y >> 16);
+        } else {
+          qf[k][0] = r0 < nrows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 32)) : 0u;
+          qf[k][2] = r0 < nrows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 32 + 16)) : 0u;
+          qf[k][1] = r0 + 8 < nrows ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 32)) : 0u;
+          qf[k][3] = r0 + 8 < nrows ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 32 + 16)) : 0u;
+        }
+      }
+    }
+    float* srow = nullptr;
+    if (SCORES && sg.own)
+      srow = a.scores + (static_cast<long long>(sg.b * a.Hkv + sg.kvh) * rows_all + first) * a.score_stride;
+    float acc[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+    for (int pg = sg.p0; pg < sg.p1; ++pg, ++it) {
+      const int st = it % C::NST;
+      if (mbar_wait(full(st), (it / C::NST) & 1, abort_flag, a.status)) {
+        const uint32_t kt = sring + st * C::STAGE, vt = kt + C::TILE;
+        const int s0 = pg * kTile + warp * 16;     // this warp's first token
+        // S = Q K^T for 16 tokens
+        float s[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+        if (FP8) {
+#pragma unroll
+          for (int k = 0; k < D / 16; k += 2) {
+            uint32_t r[4];
+            ldsm4(r, kt + k_row + (((k + k_sub) ^ sw) << 4));
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                mma16816<true>(s[j], qf[k + kk], e4m3x2_to_h2(r[2 * kk + j] & 0xFFFFu), e4m3x2_to_h2(r[2 * kk + j] >> 16));
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const int c = 2 * k + k_sub;
+            uint32_t r[4];
+            ldsm4(r, kt + (c >> 3) * C::CHUNK + k_row + (((c & 7) ^ sw) << 4));
+            mma16816<false>(s[0], qf[k], r[0], r[1]);
+            mma16816<false>(s[1], qf[k], r[2], r[3]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[j][e] *= a.scale_log2;
+        const bool edge = s0 + 16 > lim_lo;
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (s0 + j * 8 + qd * 2 + (e & 1) >= (e < 2 ? lim0 : lim1)) s[j][e] = -INFINITY;
+        }
+        if (SCORES && sg.own) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float* at = srow + s0 + j * 8 + qd * 2;
+            if (r0 < nrows) *reinterpret_cast<float2*>(at + r0 * a.score_stride) = make_float2(s[j][0], s[j][1]);
+            if (r0 + 8 < nrows)
+              *reinterpret_cast<float2*>(at + (r0 + 8) * a.score_stride) = make_float2(s[j][2], s[j][3]);
+          }
+        }
+        // running maximum (raised lazily, when it grows by more than 2^8: p <= 2^8 until then)
+        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        x0 = fmaxf(x0, __shfl_xor_sync(all, x0, 1));
+        x1 = fmaxf(x1, __shfl_xor_sync(all, x1, 1));
+        x0 = fmaxf(x0, __shfl_xor_sync(all, x0, 2));
+        x1 = fmaxf(x1, __shfl_xor_sync(all, x1, 2));
+        if (__any_sync(all, x0 > m0 + 8.0f || x1 > m1 + 8.0f)) {
+          const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+          const float a0 = n0 == m0 ? 1.0f : ex2_approx(m0 - n0), a1 = n1 == m1 ? 1.0f : ex2_approx(m1 - n1);
+          m0 = n0;
+          m1 = n1;
+          l0 *= a0;
+          l1 *= a1;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            acc[i][0] *= a0;
+            acc[i][1] *= a0;
+            acc[i][2] *= a1;
+            acc[i][3] *= a1;
+          }
+        }
+        const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          s[j][0] = ex2_approx(s[j][0] - u0);
+          s[j][1] = ex2_approx(s[j][1] - u0);
+          s[j][2] = ex2_approx(s[j][2] - u1);
+          s[j][3] = ex2_approx(s[j][3] - u1);
+        }
+        l0 += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
+        l1 += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
+        uint32_t pf[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          pf[2 * j] = FP8 ? pack_f16x2(s[j][0], s[j][1]) : pack_bf16x2(s[j][0], s[j][1]);
+          pf[2 * j + 1] = FP8 ? pack_f16x2(s[j][2], s[j][3]) : pack_bf16x2(s[j][2], s[j][3]);
+        }
+        // O += P V with V's tokens at or behind `limit` taken as zero; ONLY: into the rows
+        // flagged in w0 / w1 alone
+        auto pv = [&](auto only, bool cut, int limit, bool w0, bool w1) {
+          constexpr bool ONLY = decltype(only)::value;
+          auto mm = [&](float(&c)[4], uint32_t b0, uint32_t b1) {
+            if constexpr (!ONLY) {
+              mma16816<FP8>(c, pf, b0, b1);
+            } else {
+              float x[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816<FP8>(x, pf, b0, b1);
+              c[0] += w0 ? x[0] : 0.f;
+              c[1] += w0 ? x[1] : 0.f;
+              c[2] += w1 ? x[2] : 0.f;
+              c[3] += w1 ? x[3] : 0.f;
+            }
+          };
+          const uint32_t z0 = cut ? keep_below(s0 + qd * 2, limit) : 0xFFFFFFFFu;
+          const uint32_t z1 = cut ? keep_below(s0 + qd * 2 + 8, limit) : 0xFFFFFFFFu;
+          if (FP8) {
+#pragma unroll
+            for (int c = 0; c < D / 16; c += 2) {
+              uint32_t r[4];
+              ldsm4_t(r, vt + v_row + (((c + v_sub) ^ sw) << 4));
+#pragma unroll
+              for (int cc = 0; cc < 2; ++cc) {
+                const uint32_t x = r[2 * cc] & z0, y = r[2 * cc + 1] & z1;
+                const uint32_t xl = e4m3x2_to_h2(x & 0xFFFFu), xh = e4m3x2_to_h2(x >> 16);
+                const uint32_t yl = e4m3x2_to_h2(y & 0xFFFFu), yh = e4m3x2_to_h2(y >> 16);
+                mm(acc[2 * (c + cc)], __byte_perm(xl, xh, 0x5410), __byte_perm(yl, yh, 0x5410));
+                mm(acc[2 * (c + cc) + 1], __byte_perm(xl, xh, 0x7632), __byte_perm(yl, yh, 0x7632));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < D / 8; c += 2) {
+              uint32_t r[4];
+              const int cv = c + v_sub;
+              ldsm4_t(r, vt + (cv >> 3) * C::CHUNK + v_row + (((cv & 7) ^ sw) << 4));
+              mm(acc[c], r[0] & z0, r[1] & z1);
+              mm(acc[c + 1], r[2] & z0, r[3] & z1);
+            }
+          }
+        };
+        if (!edge) {
+          pv(std::false_type{}, false, 0, true, true);
+        } else if (lim_lo == lim_hi || lim_lo >= s0 + 16 || lim_hi <= s0) {
+          pv(std::false_type{}, true, lim_hi, true, true);
+        } else {
+          // The rows' limits differ inside these 16 tokens (drafted tokens): one product per
+          // new token, taken by its rows alone, so that a row is never touched by a V row
+          // that it does not see (0 * NaN).
+          const int ta = first / G, tb = (first + nrows - 1) / G;
+          const int mine0 = (first + min(r0, nrows - 1)) / G, mine1 = (first + min(r0 + 8, nrows - 1)) / G;
+          for (int t = ta; t <= tb; ++t)
+            pv(std::true_type{}, true, max(0, sg.len - a.n + t + 1), mine0 == t, mine1 == t);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(st));
+    }
+
+    // join the four warps' shares
+    l0 += __shfl_xor_sync(all, l0, 1);
+    l1 += __shfl_xor_sync(all, l1, 1);
+    l0 += __shfl_xor_sync(all, l0, 2);
+    l1 += __shfl_xor_sync(all, l1, 2);
+    if (qd == 0) {
+      ml[warp * 16 + r0] = make_float2(m0, l0);
+      ml[warp * 16 + r0 + 8] = make_float2(m1, l1);
+    }
+    const bool direct = sg.own && sg.p0 == 0 && sg.p1 == sg.pages && p.prt == 0;
+    const long long slot = static_cast<long long>(blockIdx.x) + sg.unit;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (8 * half >= nrows) break;
+#pragma unroll
+      for (int ch = 0; ch < D / 64; ++ch) {
+        float* mine = merge + (warp * 8 + r0) * 64;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const int x = ch * 8 + i;
+          if (FP8) {
+            *reinterpret_cast<float4*>(mine + i * 8 + qd * 4) = make_float4(
+                acc[x][2 * half], acc[x + 1][2 * half], acc[x][2 * half + 1], acc[x + 1][2 * half + 1]);
+          } else {
+            *reinterpret_cast<float2*>(mine + i * 8 + qd * 2) = make_float2(acc[x][2 * half], acc[x][2 * half + 1]);
+            *reinterpret_cast<float2*>(mine + i * 8 + 8 + qd * 2) =
+                make_float2(acc[x + 1][2 * half], acc[x + 1][2 * half + 1]);
+          }
+        }
+        consumer_sync();
+        const int rr = tid / 16, r = half * 8 + rr, col = (tid % 16) * 4;  // 8 rows x 16 groups of 4 columns
+        if (r < nrows) {
+          float M = -INFINITY;
+          float2 v[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            v[w] = ml[w * 16 + r];
+            M = fmaxf(M, v[w].x);
+          }
+          float L = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float f = v[w].x == -INFINITY ? 0.f : ex2_approx(v[w].x - M);
+            const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + rr) * 64 + col);
+            L += f * v[w].y;
+            o.x += f * x.x;
+            o.y += f * x.y;
+            o.z += f * x.z;
+            o.w += f * x.w;
+          }
+          const bool lead = ch == 0 && col == 0;
+          if (direct) {
+            const int g = row_base + r;
+            const long long tok = g / G;
+            const int h = sg.kvh * G + g % G;
+            const float inv = M == -INFINITY && L == 0.f ? 0.f : a.v_scale / L;  // nothing seen: o = 0
+            *reinterpret_cast<uint2*>(static_cast<unsigned char*>(a.out) + ((tok * a.Hq + h) * D + ch * 64 + col) * 2) =
+                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            if (a.lse != nullptr && lead)
+              a.lse[static_cast<long long>(h) * a.B * a.n + tok] =
+                  L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+          } else {
+            *reinterpret_cast<float4*>(a.part_o + (slot * a.part_rows + r) * D + ch * 64 + col) = o;
+          }
+          if (lead && (!direct || SCORES)) a.part_ml[slot * kDecodeRows + r] = make_float2(M, L);
+        }
+        consumer_sync();
+      }
+    }
+  }
+}
+
+// The partials of one row's unit: CTAs c0..c1 share tiles [u0, u0 + pages) of the line.
+struct Pieces {
+  long long slot;    // first slot; the following ones are adjacent
+  int n;
+};
+__device__ __forceinline__ Pieces pieces_of(int first_tile, int pages, int unit, int per) {
+  if (pages == 0) return Pieces{0, 0};
+  const int c0 = first_tile / per, c1 = (first_tile + pages - 1) / per;
+  return Pieces{static_cast<long long>(c0) + unit, c1 - c0 + 1};
+}
+__device__ __forceinline__ Pieces own_pieces(const DecodeParams& p, int per, int b, int base, int pages, int kvh,
+                                             int rtile) {
+  const int u = kvh * p.rt + rtile;
+  return pieces_of(base + u * pages, pages, p.a.Hkv * (p.prt + b * p.rt) + u, per);
+}
+__device__ __forceinline__ Pieces prefix_pieces(const DecodeParams& p, int per, int kvh, int row) {
+  if (p.prt == 0) return Pieces{0, 0};
+  const int u = kvh * p.prt + row / kDecodeRows;
+  return pieces_of(u * p.prefix_pages, p.prefix_pages, u, per);
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Maximum and sum over a row's partials (all lanes get both).
+__device__ __forceinline__ float2 row_stats(const DecodeArgs& a, Pieces own, int own_row, Pieces pre, int pre_row) {
+  const int lane = threadIdx.x % 32;
+  float M = -INFINITY;
+  for (int i = lane; i < own.n; i += 32) M = fmaxf(M, a.part_ml[(own.slot + i) * kDecodeRows + own_row].x);
+  for (int i = lane; i < pre.n; i += 32) M = fmaxf(M, a.part_ml[(pre.slot + i) * kDecodeRows + pre_row].x);
+  M = warp_max(M);
+  float L = 0.f;
+  auto add = [&](long long slot, int row) {
+    const float2 v = a.part_ml[slot * kDecodeRows + row];
+    if (v.x != -INFINITY) L += ex2_approx(v.x - M) * v.y;
+    else L += v.y;  // zero, or the NaN of a row whose scores are all NaN
+  };
+  for (int i = lane; i < own.n; i += 32) add(own.slot + i, own_row);
+  for (int i = lane; i < pre.n; i += 32) add(pre.slot + i, pre_row);
+  return make_float2(M, warp_sum(L));
+}
+
+// Joins the partials of rows whose keys fell to several CTAs (blocks below row_blocks, one
+// warp per row) and adds up the softmax weights (the other blocks, from the stored scores).
+template <int D, bool SCORES>
+__global__ void __launch_bounds__(kFinishThreads) decode_finish(const __grid_constant__ DecodeParams p, int row_blocks) {
+  const DecodeArgs& a = p.a;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, G = a.G, R = a.n * G;
+  __shared__ float lse2[256];
+  __shared__ int where[2];
+  pdl_wait();
+  const int total = a.cum[a.B];
+  const int per = max(1, (total + p.ctas - 1) / p.ctas);
+
+  if (static_cast<int>(blockIdx.x) < row_blocks) {
+    const long long row = static_cast<long long>(blockIdx.x) * (kFinishThreads / 32) + warp;  // token-major, then head
+    if (row >= static_cast<long long>(a.B) * a.n * a.Hq) return;
+    const int tok = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
+    const int b = tok / a.n, kvh = h / G, rr = (tok % a.n) * G + h % G, pr = b * R + rr;
+    const int base = a.cum[b], pages = (a.cum[b + 1] - base) / (a.Hkv * p.rt);
+    const Pieces own = own_pieces(p, per, b, base, pages, kvh, rr / kDecodeRows);
+    const Pieces pre = prefix_pieces(p, per, kvh, pr);
+    if (p.prt == 0 && own.n == 1) return;  // written by the CTA that saw all of it
+    const float2 st = row_stats(a, own, rr % kDecodeRows, pre, pr % kDecodeRows);
+    constexpr int E = D / 32;
+    float o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    auto add = [&](long long slot, int r) {
+      const float2 v = a.part_ml[slot * kDecodeRows + r];
+      const float f = v.x == -INFINITY ? (v.y == 0.f ? 0.f : 1.f) : ex2_approx(v.x - st.x);
+      const float* src = a.part_o + (slot * a.part_rows + r) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += f * src[e];
+    };
+#pragma unroll 4
+    for (int i = 0; i < own.n; ++i) add(own.slot + i, rr % kDecodeRows);
+#pragma unroll 4
+    for (int i = 0; i < pre.n; ++i) add(pre.slot + i, pr % kDecodeRows);
+    const float inv = st.x == -INFINITY && st.y == 0.f ? 0.f : a.v_scale / st.y;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.out) +
+                                                ((static_cast<long long>(tok) * a.Hq + h) * D + lane * E) * 2);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+    if (a.lse != nullptr && lane == 0)
+      a.lse[static_cast<long long>(h) * a.B * a.n + tok] =
+          st.y == 0.f ? -INFINITY : (st.x + log2f(st.y)) * 0.69314718055994531f;
+    return;
+  }
+
+  if constexpr (SCORES) {
+    // An equal share of the own pages of all (sequence, kv-head) pairs, in line order.
+    const int nb = gridDim.x - row_blocks, c = blockIdx.x - row_blocks;
+    const int lines = (total - p.prefix_tiles) / p.rt;
+    const int share = (lines + nb - 1) / nb;
+    int t = min(lines, c * share);
+    const int end = min(lines, t + share);
+    while (t < end) {
+      if (threadIdx.x == 0) where[0] = -1;
+      __syncthreads();
+      for (int b = threadIdx.x; b < a.B; b += kFinishThreads) {
+        const int lo = (a.cum[b] - p.prefix_tiles) / p.rt, hi = (a.cum[b + 1] - p.prefix_tiles) / p.rt;
+        if (lo <= t && t < hi) where[0] = b;
+      }
+      __syncthreads();
+      const int b = where[0];
+      const int base = a.cum[b], pages = (a.cum[b + 1] - base) / (a.Hkv * p.rt);
+      const int off = t - (base - p.prefix_tiles) / p.rt, kvh = off / pages, p0 = off % pages;
+      const int p1 = min(pages, p0 + (end - t)), len = clamp_len(a, b);
+      const long long unit = static_cast<long long>(b) * a.Hkv + kvh;
+      const float* win = a.weights_in ? a.weights_in + unit * a.weights_stride : nullptr;
+      float* wout = a.weights_out + unit * a.weights_stride;
+      for (int r0 = 0; r0 < R; r0 += 256) {
+        const int nr = min(256, R - r0);
+        for (int r = warp; r < nr; r += kFinishThreads / 32) {
+          const int rr = r0 + r, pr = b * R + rr;
+          const float2 st = row_stats(a, own_pieces(p, per, b, base, pages, kvh, rr / kDecodeRows), rr % kDecodeRows,
+                                      prefix_pieces(p, per, kvh, pr), pr % kDecodeRows);
+          // a row that sees nothing adds exp2(-inf - inf) = 0
+          if (lane == 0) lse2[r] = st.y == 0.f ? INFINITY : st.x + log2f(st.y);
+        }
+        __syncthreads();
+        const float* sc = a.scores + (unit * R + r0) * a.score_stride;
+        for (int j = p0 * kTile + threadIdx.x * 4; j < min(len, p1 * kTile); j += kFinishThreads * 4) {
+          float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+          for (int r = 0; r < nr; ++r) {
+            const float4 x = *reinterpret_cast<const float4*>(sc + r * a.score_stride + j);
+            w[0] += ex2_approx(x.x - lse2[r]);
+            w[1] += ex2_approx(x.y - lse2[r]);
+            w[2] += ex2_approx(x.z - lse2[r]);
+            w[3] += ex2_approx(x.w - lse2[r]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + e < len) {
+              const float was = r0 > 0 ? wout[j + e] : (win ? win[j + e] : 0.f);
+              wout[j + e] = was + w[e];
+            }
+        }
+        __syncthreads();
+      }
+      t += p1 - p0;
+    }
+  }
+}
+
+template <typename K, typename... A>
+cudaError_t launch_dependent(K kern, int grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int D, bool FP8, bool SCORES>
+cudaError_t run(const DecodeParams& prm, cudaStream_t st) {
+  using C = Cfg<D, FP8>;
+  cudaError_t e = set_smem_once<decode_kernel<D, FP8, SCORES>>(C::SMEM);
+  if (e != cudaSuccess) return e;
+  decode_kernel<D, FP8, SCORES><<<prm.ctas, kThreads, C::SMEM, st>>>(prm);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const DecodeArgs& a = prm.a;
+  const long long rows = static_cast<long long>(a.B) * a.n * a.Hq;
+  const int row_blocks = static_cast<int>((rows + kFinishThreads / 32 - 1) / (kFinishThreads / 32));
+  const long long pages = static_cast<long long>(a.B) * a.Hkv * ((a.max_kv_len + kTile - 1) / kTile);
+  const int weight_blocks = SCORES ? static_cast<int>(pages < 2 * kDecodeCtas ? pages : 2 * kDecodeCtas) : 0;
+  return launch_dependent(decode_finish<D, SCORES>, row_blocks + weight_blocks, kFinishThreads, 0, st, prm, row_blocks);
+}
+
+}  // namespace
+
+cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st) {
+  DecodeParams prm;
+  memset(&prm, 0, sizeof(prm));
+  const int box_d = fp8 ? 128 : 64;
+  const long long kv_rows = static_cast<long long>(a.num_slots) * kTile;
+  if (!make_map(&prm.tk, a.k_cache, fp8, a.d, a.Hkv, kv_rows, box_d, kTile)) return cudaErrorInvalidValue;
+  if (!make_map(&prm.tv, a.v_cache, fp8, a.d, a.Hkv, kv_rows, box_d, kTile)) return cudaErrorInvalidValue;
+  prm.a = a;
+  const int R = a.n * a.G;
+  prm.rt = (R + kDecodeRows - 1) / kDecodeRows;
+  prm.prt = a.prefix_len > 0 ? (a.B * R + kDecodeRows - 1) / kDecodeRows : 0;
+  prm.prefix_pages = (a.prefix_len + kTile - 1) / kTile;
+  prm.prefix_tiles = a.Hkv * prm.prt * prm.prefix_pages;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const long long bound =
+      prm.prefix_tiles + static_cast<long long>(a.B) * a.Hkv * prm.rt * ((a.max_kv_len + kTile - 1) / kTile);
+  prm.ctas = 2 * sms < kDecodeCtas ? 2 * sms : kDecodeCtas;
+  if (bound < prm.ctas) prm.ctas = static_cast<int>(bound);
+  const bool scores = a.scores != nullptr;
+  if (fp8) return scores ? run<128, true, true>(prm, st) : run<128, true, false>(prm, st);
+  if (a.d == 128) return scores ? run<128, false, true>(prm, st) : run<128, false, false>(prm, st);
+  return scores ? run<64, false, true>(prm, st) : run<64, false, false>(prm, st);
+}
+
+}  // namespace stem

@@ -432,6 +432,52 @@ struct BsaArgs {
 cudaError_t launch_bsa(const Batch& bt, const BsaArgs& a, bool fp8, bool paged, bool dense, uint32_t* status,
                        cudaStream_t st);
 
+// Tensor map over a token-major [rows, H, d] tensor: dims (d, H, rows), box (box_d, 1,
+// box_rows), 128-byte swizzle.  False when the driver refuses it.
+bool make_map(CUtensorMap* m, const void* ptr, bool fp8, int d, int H, long long rows, int box_d, int box_rows);
+
+// Split of one decoding step over the CTAs.  The step's work is a line of 64-token tiles:
+// the prefix's units (kv-head, 16-row tile of all sequences' rows), then sequence after
+// sequence its own (kv-head, 16-row tile) units; every unit is as many tiles as its keys
+// have pages, and CTA c takes tiles [c * per, (c + 1) * per).
+constexpr int kDecodeCtas = 296;      // two on each of 148 SMs
+constexpr int kDecodeRows = 16;       // query rows of a unit
+
+struct DecodeArgs {
+  const void* q;
+  const int32_t* kv_lens;
+  const int32_t* table;
+  const int32_t* prefix_table;
+  const void* k_cache;
+  const void* v_cache;
+  int max_pages, num_slots;
+  int B, n, Hq, Hkv, G, d;
+  int max_kv_len, prefix_len;
+  float scale_log2;          // sigma * q_scale * k_scale * log2(e)
+  float v_scale;             // 1 for BF16
+  const float* weights_in;
+  float* weights_out;
+  long long weights_stride;
+  void* out;
+  float* lse;
+  // workspace
+  uint32_t* status;
+  int32_t* cum;              // [B + 1] first tile of each sequence
+  float* part_o;             // [slots, part_rows, d] unnormalised outputs of a CTA's share of a unit
+  float2* part_ml;           // [slots, 16] running maximum (log2 domain) and sum
+  float* scores;             // [B, Hkv, n * G, score_stride] log2-domain scores, or nullptr
+  long long score_stride;
+  int part_rows;
+};
+
+struct DecodeWs {
+  size_t status, cum, part_ml, part_o, scores, total;
+  int part_rows;
+  long long score_stride;
+};
+
+cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st);
+
 // Pending failure-injection request (stem_debug_inject); consumed by the next BSA launch.
 int take_injection();
 void set_injection(int mode);

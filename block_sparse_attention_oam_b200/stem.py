@@ -61,6 +61,24 @@ class _Paged(ctypes.Structure):
     ]
 
 
+class _Decode(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int),
+        ("q_len", ctypes.c_int),
+        ("num_q_heads", ctypes.c_int),
+        ("num_kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("q_scale", ctypes.c_float),
+        ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+        ("softmax_scale", ctypes.c_float),
+        ("max_kv_len", ctypes.c_int),
+        ("prefix_len", ctypes.c_int),
+        ("collect_weights", ctypes.c_int),
+    ]
+
+
 class _Sizes(ctypes.Structure):
     _fields_ = [
         ("num_rows", ctypes.c_int64),
@@ -100,6 +118,9 @@ def lib() -> ctypes.CDLL:
         "stem_attention_noalloc": ([pp, _P, _P, _P, pg, _P, _P, _P, _P, _P, _P], ctypes.c_int),
         "stem_attention_host": ([pp, _P, _P, _P, _P, _P, _P, pg, _P, _P, _P, _P, _P, ctypes.c_int, _P,
                                  ctypes.c_size_t, _P], ctypes.c_int),
+        "stem_decode_workspace_size": ([ctypes.POINTER(_Decode)], ctypes.c_size_t),
+        "stem_decode": ([ctypes.POINTER(_Decode), _P, pg, _P, _P, _P, _P, ctypes.c_int64, _P, _P, _P, ctypes.c_size_t,
+                         _P], ctypes.c_int),
         "stem_query_status": ([_P, _P], ctypes.c_int),
         "stem_reset_status": ([_P, _P], ctypes.c_int),
         "stem_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -325,6 +346,110 @@ def stem_attention_noalloc(prob: Problem, q, k, v, paged: Optional[PagedKV] = No
     out = _out(prob, q, out)
     _check(lib().stem_attention_noalloc(prob.c, _ptr(q), _ptr(k), _ptr(v), _paged(paged), _ptr(out), _ptr(lse),
                                         _ptr(row_ptr), _ptr(col_idx), _ptr(status), _stream(stream)))
+    return out
+
+
+@dataclasses.dataclass
+class Decode:
+    """One decoding step: the newest q_len tokens of num_seqs sequences over a paged cache
+    (stem_decode_t).  The numbers are taken when the object is made."""
+    num_seqs: int
+    num_q_heads: int
+    num_kv_heads: int
+    head_dim: int
+    max_kv_len: int
+    q_len: int = 1
+    dtype: str = "bf16"
+    q_scale: float = 1.0
+    k_scale: float = 1.0
+    v_scale: float = 1.0
+    softmax_scale: float = 0.0
+    prefix_len: int = 0          # tokens of a prefix that all sequences share
+    weights: bool = False        # also add up the softmax weights of every cached token
+
+    def __post_init__(self):
+        self._c = _Decode(self.num_seqs, self.q_len, self.num_q_heads, self.num_kv_heads, self.head_dim,
+                          _dtype_code(self.dtype), self.q_scale, self.k_scale, self.v_scale, self.softmax_scale,
+                          self.max_kv_len, self.prefix_len, 1 if self.weights else 0)
+        self._torch = _TORCH_DTYPES[self.dtype]
+
+    @property
+    def c(self):
+        return ctypes.byref(self._c)
+
+    def workspace_bytes(self) -> int:
+        n = lib().stem_decode_workspace_size(self.c)
+        if n == 0:
+            raise StemError(STEM_ERR_INVALID, lib().stem_last_error().decode())
+        return n
+
+
+_TORCH_DTYPES = {"bf16": torch.bfloat16, "fp8_e4m3": torch.float8_e4m3fn}
+
+
+def _dtype_code(name: str) -> int:
+    if name not in _TORCH_DTYPES:
+        raise ValueError(f"dtype {name!r} (supported: {', '.join(_TORCH_DTYPES)})")
+    return DT_FP8 if name == "fp8_e4m3" else DT_BF16
+
+
+def _tensor(name: str, t, shape, dtype, device):
+    """A dense tensor of this shape (None: any length), type and device."""
+    if t.dtype != dtype or t.device != device or t.dim() != len(shape) or not t.is_contiguous() or any(
+            w is not None and w != g for w, g in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}; got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _pages(name: str, c: PagedKV, num_seqs: int, Hkv: int, d: int, dtype, device):
+    shape = (None, PAGE_SIZE, Hkv, d)
+    k = _tensor(f"{name}.k_cache", c.k_cache, shape, dtype, device)
+    v = _tensor(f"{name}.v_cache", c.v_cache, tuple(c.k_cache.shape), dtype, device)
+    t = _tensor(f"{name}.block_table", c.block_table, (num_seqs, None), torch.int32, device)
+    return ctypes.byref(_Paged(k, v, t, PAGE_SIZE, c.block_table.shape[1], c.k_cache.shape[0]))
+
+
+def _call_on(device, stream, fn, *args) -> None:
+    """Call the library on the tensors' device, on `stream` or that device's current one."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call_on(device, stream, fn, *args)
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    _check(fn(*args, s.cuda_stream))
+
+
+def decode_workspace(dec: Decode, device="cuda") -> torch.Tensor:
+    return torch.zeros(dec.workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def stem_decode(dec: Decode, q, cache: PagedKV, kv_lens, prefix_table=None, weights_in=None, weights_out=None,
+                out=None, lse=None, ws=None, stream=None):
+    """Attention of the newest tokens q [num_seqs * q_len, Hq, d] over the paged cache, of
+    which sequence b holds kv_lens[b] tokens (device int32, the new ones among them), after
+    the shared prefix of prefix_table's pages where dec.prefix_len > 0.  dec.weights:
+    weights_out [num_seqs, Hkv, stride] = weights_in + the softmax weights of each token.
+    Returns out (bf16); lse: float [Hq, num_seqs * q_len], written if given."""
+    B, n, Hq, Hkv, d, dev = dec.num_seqs, dec.q_len, dec.num_q_heads, dec.num_kv_heads, dec.head_dim, q.device
+    if dev.type != "cuda":
+        raise ValueError("stem_decode takes CUDA tensors")
+    if out is None:
+        out = torch.empty((B * n, Hq, d), dtype=torch.bfloat16, device=dev)
+    if ws is None:
+        ws = decode_workspace(dec, dev)
+    if dec.weights != (weights_out is not None) or (weights_in is not None and weights_out is None):
+        raise ValueError("weights_out goes with Decode(weights=True), weights_in with weights_out")
+    stride = weights_out.shape[-1] if dec.weights else 0
+    ok = torch.float32
+    _call_on(dev, stream, lib().stem_decode, dec.c, _tensor("q", q, (B * n, Hq, d), dec._torch, dev),
+             _pages("cache", cache, B, Hkv, d, dec._torch, dev), _tensor("kv_lens", kv_lens, (B,), torch.int32, dev),
+             None if prefix_table is None else _tensor("prefix_table", prefix_table, (-(-dec.prefix_len // PAGE_SIZE),),
+                                                       torch.int32, dev),
+             None if weights_in is None else _tensor("weights_in", weights_in, (B, Hkv, stride), ok, dev),
+             None if weights_out is None else _tensor("weights_out", weights_out, (B, Hkv, stride), ok, dev), stride,
+             _tensor("out", out, (B * n, Hq, d), torch.bfloat16, dev),
+             None if lse is None else _tensor("lse", lse, (Hq, B * n), ok, dev),
+             _tensor("ws", ws, (None,), torch.uint8, dev), ws.numel())
     return out
 
 

@@ -267,6 +267,65 @@ STEM_API stem_status_t stem_attention_noalloc(const stem_problem_t* prob, const 
                                               int32_t* row_ptr_out, int32_t* col_idx_out, uint32_t* status_out,
                                               void* stream);
 
+/* ------------------------------------------------------------------ decoding
+ * After the prefill: attention of the newest tokens over the paged cache, and eviction
+ * from it.  The pages describe the prefill only; these operators are this library's own,
+ * over the same cache layout.
+ */
+#define STEM_MAX_DECODE_SEQS 1024
+#define STEM_MAX_Q_LEN 64
+#define STEM_MAX_KV_LEN (STEM_MAX_BLOCKS * 128)
+
+/* One decoding step: the newest q_len tokens of every sequence of a batch. */
+typedef struct {
+  int num_seqs;                /* B, at most STEM_MAX_DECODE_SEQS; a padded batch gives its idle rows length 0 */
+  int q_len;                   /* new tokens per sequence: 1, or more where drafted tokens are checked; at most STEM_MAX_Q_LEN */
+  int num_q_heads;             /* Hq */
+  int num_kv_heads;            /* Hkv; q-head h reads kv-head h / (Hq/Hkv) */
+  int head_dim;                /* d: 64 or 128 (FP8: 128) */
+  stem_dtype_t dtype;          /* storage type of Q and of the cache */
+  float q_scale, k_scale, v_scale; /* FP8: value = code * scale (per tensor); BF16: ignored */
+  float softmax_scale;         /* sigma; <= 0 selects 1/sqrt(head_dim) */
+  int max_kv_len;              /* no kv_lens entry exceeds it; 1..STEM_MAX_KV_LEN */
+  int prefix_len;              /* tokens of a prefix that all sequences share, 0: none; at most STEM_MAX_KV_LEN */
+  int collect_weights;         /* 1: also add up the softmax weights each cached token receives */
+} stem_decode_t;
+
+/* Device workspace bytes of stem_decode (0 on a bad problem).  Host only. */
+STEM_API size_t stem_decode_workspace_size(const stem_decode_t* dec);
+
+/*
+ * Attention of the newest tokens over a paged cache.  Row (b, t, h), t < q_len, sees the
+ * shared prefix (all of it) and the sequence's own tokens j < kv_lens[b] - q_len + t + 1
+ * (its K/V, the new tokens' included, are in the cache already):
+ *   o = sum_j softmax_j(sigma q.k_j) v_j,   lse = ln sum_j exp(sigma q.k_j);
+ * a row that sees nothing gets o = 0 and lse = -inf.  Rows of K and V that no row sees
+ * (the rest of a last page, tokens behind a drafted one) may hold anything, NaN included.
+ * q: DEVICE [B * q_len, Hq, d], 16-byte aligned.  out: DEVICE bf16 [B * q_len, Hq, d].
+ * lse: DEVICE float [Hq, B * q_len] (natural log), or NULL.
+ * cache: the pages of the sequences' own tokens (required).  kv_lens: DEVICE int32 [B],
+ *   0..max_kv_len, read on the device (a captured graph may be replayed as they grow); a
+ *   value outside is clamped and reported as STEM_ERR_BOUNDS, as is a page outside the
+ *   cache, which is read as slot 0.
+ * prefix_table: DEVICE int32 [ceil(prefix_len / 64)] slots of the prefix in the same
+ *   cache, or NULL with prefix_len 0.  The prefix is read once for the whole batch, and
+ *   kv_lens count only the tokens behind it.
+ * weights_in, weights_out (collect_weights 1): DEVICE float [B, Hkv, weights_stride],
+ *   weights_stride >= max_kv_len:
+ *     weights_out[b, kh, j] = weights_in[b, kh, j] + sum of token j's softmax weight over
+ *   the q_len rows of the q-heads that read kv-head kh, for j < kv_lens[b]; entries behind
+ *   are left as they were.  weights_in may be NULL (zeros) or weights_out itself, and must not overlap it
+ *   otherwise.  The prefix's weights are not collected.  collect_weights 0: both NULL.
+ * ws: DEVICE workspace of ws_bytes >= stem_decode_workspace_size(), its first 256 bytes
+ *   zero before its first use (stem_reset_status).  Calls that may overlap on the GPU
+ *   (other streams, graphs replayed side by side) each need a workspace of their own.
+ * Sums and softmax statistics are float32; the result does not depend on timing.
+ */
+STEM_API stem_status_t stem_decode(const stem_decode_t* dec, const void* q, const stem_paged_kv_t* cache,
+                                   const int32_t* kv_lens, const int32_t* prefix_table, const float* weights_in,
+                                   float* weights_out, int64_t weights_stride, void* out, float* lse, void* ws,
+                                   size_t ws_bytes, void* stream);
+
 /*
  * Synchronise the stream, read and clear the device status word kept in the
  * workspace.  Returns STEM_OK, STEM_ERR_TIMEOUT, STEM_ERR_BOUNDS or STEM_ERR_CUDA.

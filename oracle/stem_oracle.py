@@ -296,3 +296,56 @@ def stem_sequence(q, k, v, block: int, keep: float, mu: float, beta: float, sigm
     out, lse = attend(q, k, v, lists, block, sigma, rows)
     return dict(qbar=qbar, kbar=kbar, lbar=lbar, scores=s, r_start=r, total=K, k=kk,
                 lists=lists, out=out, lse=lse)
+
+
+# ---------------------------------------------------------------------------
+# Decoding over a paged cache — this library's own operators, not in the pages.
+# ---------------------------------------------------------------------------
+def gather_pages(cache, slots, n: int) -> np.ndarray:
+    """The first n tokens of a page list: cache [num_slots, P, H, d] -> [n, H, d]."""
+    P = cache.shape[1]
+    return np.concatenate([cache[s] for s in slots[: -(-n // P)]] + [cache[0][:0]])[:n]
+
+
+def decode_rows(q, k, v, sigma: float, prefix: int = 0):
+    """The newest n tokens of one sequence.  q [n,Hq,d]; k, v [prefix + S, Hkv, d], the
+    shared prefix first, then the sequence's own S tokens (the new ones last, S < n: the
+    first rows see no own token).  Row t sees the prefix and own tokens j < S - n + t + 1.
+    Returns out [n,Hq,d] (0 where nothing is seen), lse [Hq,n] (-inf there), the weights
+    summed over rows and the q-heads of a group [Hkv,S], and what error bounds need: the
+    weighted mean of |v| [n,Hq,d] and sigma * sum_i |q_i k_i| at its largest [n,Hq]."""
+    n, Hq, d = q.shape
+    Hkv = k.shape[1]
+    g = Hq // Hkv
+    S = k.shape[0] - prefix
+    out, lse = np.zeros((n, Hq, d)), np.full((Hq, n), -np.inf)
+    weights, mean_abs, size = np.zeros((Hkv, S)), np.zeros((n, Hq, d)), np.zeros((n, Hq))
+    for t in range(n):
+        see = prefix + max(0, S - n + t + 1)
+        if see == 0:
+            continue
+        for h in range(Hq):
+            kh = h // g
+            logits = sigma * (k[:see, kh] @ q[t, h])
+            m = logits.max()
+            p = np.exp(logits - m)
+            lse[h, t] = m + np.log(p.sum())
+            p = p / p.sum()
+            out[t, h] = p @ v[:see, kh]
+            mean_abs[t, h] = p @ np.abs(v[:see, kh])
+            size[t, h] = sigma * (np.abs(k[:see, kh]) @ np.abs(q[t, h])).max()
+            weights[kh, : see - prefix] += p[prefix:]
+    return out, lse, weights, mean_abs, size
+
+
+def evict_keep(weights, n: int, budget: int, sink: int, recent: int) -> np.ndarray:
+    """Tokens kept of n (ascending): all where n <= budget, else the first `sink`, the last
+    `recent` and of the others those of the largest weight, ties to the lower index; a NaN
+    weight ranks as -inf."""
+    if n <= budget:
+        return np.arange(n)
+    mid = np.arange(sink, n - recent)
+    w = np.asarray(weights, dtype=np.float64)[mid]
+    w = np.where(np.isnan(w), -np.inf, w)
+    best = mid[np.lexsort((mid, -w))][: budget - sink - recent]
+    return np.sort(np.concatenate([np.arange(sink), best, np.arange(n - recent, n)])).astype(np.int64)

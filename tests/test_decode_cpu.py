@@ -1,0 +1,141 @@
+"""Decoding operators without a GPU: every refusal happens on the host before any CUDA
+call, workspace sizes follow the problem, and the oracle's rows and eviction rule are
+pinned by hand."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_attention_oam_b200 import build as B
+from block_sparse_attention_oam_b200 import stem as S
+from oracle import stem_oracle as O
+
+
+@pytest.fixture(scope="module")
+def L():
+    B.build()
+    return S.lib()
+
+
+FAKE = ctypes.c_void_p(0x1000)      # never dereferenced: validation fails first
+GOOD = dict(num_seqs=3, num_q_heads=8, num_kv_heads=2, head_dim=128, max_kv_len=1000)
+
+
+def paged(max_pages=16, slots=64, page=64, k=0x1000, v=0x1000, table=0x1000):
+    return S._Paged(k, v, table, page, max_pages, slots)
+
+
+def decode(L, dec, q=FAKE, cache=None, lens=FAKE, ptable=None, w_in=None, w_out=None, stride=0, out=FAKE, ws=FAKE,
+           ws_bytes=1 << 40):
+    cache = paged() if cache is None else cache
+    return L.stem_decode(dec.c, q, ctypes.byref(cache) if cache else None, lens, ptable, w_in, w_out, stride, out,
+                         None, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(num_seqs=0), S.STEM_ERR_INVALID),
+    (dict(num_seqs=1025), S.STEM_ERR_INVALID),
+    (dict(num_q_heads=7), S.STEM_ERR_INVALID),
+    (dict(num_q_heads=0), S.STEM_ERR_INVALID),
+    (dict(num_kv_heads=0), S.STEM_ERR_INVALID),
+    (dict(num_q_heads=258), S.STEM_ERR_UNSUPPORTED),
+    (dict(head_dim=96), S.STEM_ERR_UNSUPPORTED),
+    (dict(head_dim=64, dtype="fp8_e4m3"), S.STEM_ERR_UNSUPPORTED),
+    (dict(q_len=0), S.STEM_ERR_INVALID),
+    (dict(q_len=65), S.STEM_ERR_INVALID),
+    (dict(max_kv_len=0), S.STEM_ERR_INVALID),
+    (dict(max_kv_len=262145), S.STEM_ERR_INVALID),
+    (dict(prefix_len=-1), S.STEM_ERR_INVALID),
+    (dict(prefix_len=262145), S.STEM_ERR_INVALID),
+    (dict(dtype="fp8_e4m3", k_scale=0.0), S.STEM_ERR_INVALID),
+    (dict(dtype="fp8_e4m3", v_scale=float("nan")), S.STEM_ERR_INVALID),
+    (dict(softmax_scale=float("inf")), S.STEM_ERR_INVALID),
+    (dict(num_seqs=1024, num_q_heads=256, num_kv_heads=256, max_kv_len=262144, q_len=64), S.STEM_ERR_UNSUPPORTED),
+])
+def test_decode_refuses_bad_problems(L, change, status):
+    dec = S.Decode(**(GOOD | change))
+    assert decode(L, dec, cache=paged(max_pages=1 << 20)) == status
+    assert L.stem_decode_workspace_size(dec.c) == 0
+    with pytest.raises(S.StemError):
+        dec.workspace_bytes()
+
+
+def test_decode_refuses_bad_buffers(L):
+    dec = S.Decode(**GOOD)
+    odd = ctypes.c_void_p(0x1008)
+    assert L.stem_decode(None, FAKE, ctypes.byref(paged()), FAKE, None, None, None, 0, FAKE, None, FAKE, 1 << 40, None) == S.STEM_ERR_INVALID
+    assert decode(L, dec, cache=False) == S.STEM_ERR_INVALID
+    assert decode(L, dec, q=None) == S.STEM_ERR_INVALID
+    assert decode(L, dec, q=odd) == S.STEM_ERR_INVALID
+    assert decode(L, dec, out=None) == S.STEM_ERR_INVALID
+    assert decode(L, dec, out=odd) == S.STEM_ERR_INVALID
+    assert decode(L, dec, lens=None) == S.STEM_ERR_INVALID
+    assert decode(L, dec, cache=paged(k=0)) == S.STEM_ERR_INVALID
+    assert decode(L, dec, cache=paged(v=0x1004)) == S.STEM_ERR_INVALID
+    assert decode(L, dec, cache=paged(page=32)) == S.STEM_ERR_UNSUPPORTED
+    assert decode(L, dec, cache=paged(max_pages=15)) == S.STEM_ERR_INVALID
+    assert decode(L, dec, cache=paged(slots=0)) == S.STEM_ERR_INVALID
+    assert decode(L, dec, ptable=FAKE) == S.STEM_ERR_INVALID                      # no prefix
+    assert decode(L, S.Decode(**GOOD, prefix_len=5)) == S.STEM_ERR_INVALID        # no prefix pages
+    assert decode(L, dec, w_out=FAKE, stride=1000) == S.STEM_ERR_INVALID          # weights not asked for
+    w = S.Decode(**GOOD, weights=True)
+    assert decode(L, w) == S.STEM_ERR_INVALID
+    assert decode(L, w, w_out=FAKE, stride=999) == S.STEM_ERR_INVALID
+    assert decode(L, w, w_out=FAKE, w_in=ctypes.c_void_p(0x1010), stride=1000) == S.STEM_ERR_INVALID
+    assert b"overlap" in L.stem_last_error()
+    assert decode(L, dec, ws=None) == S.STEM_ERR_WORKSPACE
+    assert decode(L, dec, ws=ctypes.c_void_p(0x1010)) == S.STEM_ERR_WORKSPACE
+    assert decode(L, dec, ws_bytes=dec.workspace_bytes() - 1) == S.STEM_ERR_WORKSPACE
+
+
+def test_decode_workspace_grows_with_the_problem(L):
+    base = S.Decode(**GOOD).workspace_bytes()
+    assert S.Decode(**(GOOD | dict(num_seqs=30))).workspace_bytes() > base
+    assert S.Decode(**GOOD, prefix_len=100).workspace_bytes() > base
+    # scores of every row and cached token, in float32
+    assert S.Decode(**GOOD, weights=True).workspace_bytes() >= base + 3 * 8 * 1024 * 4
+
+
+def test_decode_binding_checks_tensors(L):
+    dec = S.Decode(**GOOD)
+    q = torch.zeros((3, 8, 128), dtype=torch.bfloat16)
+    cache = S.PagedKV(torch.zeros((4, 64, 2, 128), dtype=torch.bfloat16), torch.zeros((4, 64, 2, 128), dtype=torch.bfloat16), torch.zeros((3, 16), dtype=torch.int32))
+    with pytest.raises(ValueError, match="CUDA"):
+        S.stem_decode(dec, q, cache, torch.zeros(3, dtype=torch.int32))
+    dev = q.device
+    with pytest.raises(ValueError, match="q must be"):
+        S._tensor("q", q[:, ::2], (3, 4, 128), torch.bfloat16, dev)
+    with pytest.raises(ValueError, match="q must be"):
+        S._tensor("q", q, (3, 8, 64), torch.bfloat16, dev)
+    with pytest.raises(ValueError, match="q must be"):
+        S._tensor("q", q.float(), (3, 8, 128), torch.bfloat16, dev)
+    with pytest.raises(ValueError, match="block_table"):
+        S._pages("cache", cache, 4, 2, 128, torch.bfloat16, dev)
+    with pytest.raises(ValueError, match="dtype"):
+        S.Decode(**GOOD, dtype="fp16")
+
+
+def test_oracle_decode_rows_by_hand():
+    """Two keys of equal score: the mean of their values; a row that sees one key, that value;
+    a row that sees nothing, zero."""
+    q = np.ones((3, 1, 2))
+    k = np.array([[[1.0, 0.0]], [[0.0, 1.0]]])
+    v = np.array([[[2.0, 0.0]], [[4.0, 6.0]]])
+    out, lse, w, _, _ = O.decode_rows(q, k, v, 1.0)
+    assert np.allclose(out[:, 0], [[0, 0], [2, 0], [3, 3]])
+    assert np.isneginf(lse[0, 0]) and np.allclose(lse[0, 1:], [1.0, 1.0 + np.log(2)])
+    assert np.allclose(w, [[1.5, 0.5]])
+    # the same two keys, the first as a shared prefix: every row sees it
+    out, lse, w, _, _ = O.decode_rows(q[:2], k, v, 1.0, prefix=1)
+    assert np.allclose(out[:, 0], [[2, 0], [3, 3]]) and np.allclose(w, [[0.5]])
+
+
+def test_oracle_agrees_with_its_own_prefill():
+    rng = np.random.default_rng(0)
+    q, k, v = rng.standard_normal((100, 4, 8)), rng.standard_normal((100, 2, 8)), rng.standard_normal((100, 2, 8))
+    lists = [[[0, 1][: i + 1] for i in range(2)] for _ in range(4)]
+    out, lse = O.attend(q, k, v, lists, 64, 0.3)
+    got, got_lse, w, _, _ = O.decode_rows(q[97:], k, v, 0.3)
+    assert np.allclose(got, out[97:]) and np.allclose(got_lse, lse[:, 97:])
+    assert np.allclose(w.sum(1), 3 * 2)          # every row's weights add up to one
