@@ -77,6 +77,18 @@ stem_status_t check_decode(const stem_decode_t* de) {
   return STEM_OK;
 }
 
+stem_status_t check_evict(const stem_evict_t* ev) {
+  if (ev == nullptr) return set_last_error(STEM_ERR_INVALID, "evict problem is NULL");
+  stem_status_t s = check_shape(ev->num_seqs, ev->num_kv_heads, ev->head_dim, ev->dtype, ev->max_kv_len);
+  if (s != STEM_OK) return s;
+  if (ev->budget < 1 || ev->budget > STEM_MAX_KV_LEN)
+    return set_last_error(STEM_ERR_INVALID, "budget %d outside [1, %d]", ev->budget, STEM_MAX_KV_LEN);
+  if (ev->sink < 0 || ev->recent < 0 || ev->sink > ev->budget || ev->recent > ev->budget - ev->sink)
+    return set_last_error(STEM_ERR_INVALID, "sink %d and recent %d must be >= 0 and fit the budget %d", ev->sink,
+                          ev->recent, ev->budget);
+  return STEM_OK;
+}
+
 DecodeWs layout(const stem_decode_t* de) {
   DecodeWs w{};
   const size_t B = de->num_seqs, Hkv = de->num_kv_heads, d = de->head_dim;
@@ -187,6 +199,65 @@ stem_status_t stem_decode(const stem_decode_t* dec, const void* q, const stem_pa
   a.part_rows = w.part_rows;
   const cudaError_t e = launch_decode(a, fp8, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return set_last_error(STEM_ERR_CUDA, "decode: %s", cudaGetErrorString(e));
+  return STEM_OK;
+}
+
+size_t stem_evict_workspace_size(const stem_evict_t* ev) { return check_evict(ev) == STEM_OK ? 256 : 0; }
+
+stem_status_t stem_evict(const stem_evict_t* ev, const stem_paged_kv_t* src, const int32_t* kv_lens,
+                         const float* weights, int64_t weights_stride, const stem_paged_kv_t* dst,
+                         int32_t* kv_lens_out, float* weights_out, int64_t weights_out_stride, int32_t* keep, void* ws,
+                         size_t ws_bytes, void* stream) {
+  stem_status_t s = check_evict(ev);
+  if (s == STEM_OK) s = check_cache(src, "src", ev->max_kv_len);
+  if (s == STEM_OK) s = check_cache(dst, "dst", ev->budget < ev->max_kv_len ? ev->budget : ev->max_kv_len);
+  if (s != STEM_OK) return s;
+  if (kv_lens == nullptr || weights == nullptr || kv_lens_out == nullptr || keep == nullptr)
+    return set_last_error(STEM_ERR_INVALID, "kv_lens, weights, kv_lens_out and keep must not be NULL");
+  if (weights_stride < ev->max_kv_len)
+    return set_last_error(STEM_ERR_INVALID, "weights_stride %lld is smaller than max_kv_len %d",
+                          static_cast<long long>(weights_stride), ev->max_kv_len);
+  const size_t units = static_cast<size_t>(ev->num_seqs) * ev->num_kv_heads;
+  const size_t lens = static_cast<size_t>(ev->num_seqs) * 4;
+  if (overlap(kv_lens, lens, kv_lens_out, lens))
+    return set_last_error(STEM_ERR_INVALID, "kv_lens_out must not overlap kv_lens");
+  if (weights_out != nullptr) {
+    if (weights_out_stride < ev->budget)
+      return set_last_error(STEM_ERR_INVALID, "weights_out_stride %lld is smaller than the budget %d",
+                            static_cast<long long>(weights_out_stride), ev->budget);
+    if (overlap(weights, units * weights_stride * 4, weights_out, units * weights_out_stride * 4))
+      return set_last_error(STEM_ERR_INVALID, "weights_out must not overlap weights");
+  }
+  if ((s = check_ws(ws, ws_bytes, 256)) != STEM_OK) return s;
+  EvictArgs a{};
+  a.kv_lens = kv_lens;
+  a.weights = weights;
+  a.weights_stride = weights_stride;
+  a.src_k = src->k_cache;
+  a.src_v = src->v_cache;
+  a.src_table = src->block_table;
+  a.src_max_pages = src->max_pages_per_seq;
+  a.src_slots = src->num_slots;
+  a.dst_k = const_cast<void*>(dst->k_cache);
+  a.dst_v = const_cast<void*>(dst->v_cache);
+  a.dst_table = dst->block_table;
+  a.dst_max_pages = dst->max_pages_per_seq;
+  a.dst_slots = dst->num_slots;
+  a.B = ev->num_seqs;
+  a.Hkv = ev->num_kv_heads;
+  const int row_bytes = ev->head_dim * (ev->dtype == STEM_DT_FP8_E4M3 ? 1 : 2);
+  a.row_shift = row_bytes == 256 ? 4 : 3;  // 128 bytes otherwise: d 64 in BF16, d 128 in FP8
+  a.max_kv_len = ev->max_kv_len;
+  a.budget = ev->budget;
+  a.sink = ev->sink;
+  a.recent = ev->recent;
+  a.kv_lens_out = kv_lens_out;
+  a.weights_out = weights_out;
+  a.weights_out_stride = weights_out_stride;
+  a.keep = keep;
+  a.status = at<uint32_t>(ws, 0);
+  const cudaError_t e = launch_evict(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return set_last_error(STEM_ERR_CUDA, "evict: %s", cudaGetErrorString(e));
   return STEM_OK;
 }
 

@@ -478,6 +478,30 @@ struct DecodeWs {
 
 cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st);
 
+struct EvictArgs {
+  const int32_t* kv_lens;
+  const float* weights;      // [B, Hkv, weights_stride]
+  long long weights_stride;
+  const void* src_k;
+  const void* src_v;
+  const int32_t* src_table;
+  int src_max_pages, src_slots;
+  void* dst_k;
+  void* dst_v;
+  const int32_t* dst_table;
+  int dst_max_pages, dst_slots;
+  int B, Hkv;
+  int row_shift;             // log2 of the 16-byte pieces of a row of one head
+  int max_kv_len, budget, sink, recent;
+  int32_t* kv_lens_out;
+  float* weights_out;        // or nullptr
+  long long weights_out_stride;
+  int32_t* keep;             // [B, Hkv, budget]
+  uint32_t* status;
+};
+
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st);
+
 // Pending failure-injection request (stem_debug_inject); consumed by the next BSA launch.
 int take_injection();
 void set_injection(int mode);

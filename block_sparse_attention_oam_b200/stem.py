@@ -79,6 +79,19 @@ class _Decode(ctypes.Structure):
     ]
 
 
+class _Evict(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int),
+        ("num_kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("max_kv_len", ctypes.c_int),
+        ("budget", ctypes.c_int),
+        ("sink", ctypes.c_int),
+        ("recent", ctypes.c_int),
+    ]
+
+
 class _Sizes(ctypes.Structure):
     _fields_ = [
         ("num_rows", ctypes.c_int64),
@@ -121,6 +134,9 @@ def lib() -> ctypes.CDLL:
         "stem_decode_workspace_size": ([ctypes.POINTER(_Decode)], ctypes.c_size_t),
         "stem_decode": ([ctypes.POINTER(_Decode), _P, pg, _P, _P, _P, _P, ctypes.c_int64, _P, _P, _P, ctypes.c_size_t,
                          _P], ctypes.c_int),
+        "stem_evict_workspace_size": ([ctypes.POINTER(_Evict)], ctypes.c_size_t),
+        "stem_evict": ([ctypes.POINTER(_Evict), pg, _P, _P, ctypes.c_int64, pg, _P, _P, ctypes.c_int64, _P, _P,
+                        ctypes.c_size_t, _P], ctypes.c_int),
         "stem_query_status": ([_P, _P], ctypes.c_int),
         "stem_reset_status": ([_P, _P], ctypes.c_int),
         "stem_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -451,6 +467,66 @@ def stem_decode(dec: Decode, q, cache: PagedKV, kv_lens, prefix_table=None, weig
              None if lse is None else _tensor("lse", lse, (Hq, B * n), ok, dev),
              _tensor("ws", ws, (None,), torch.uint8, dev), ws.numel())
     return out
+
+
+@dataclasses.dataclass
+class Evict:
+    """One eviction: every (sequence, kv-head) cut to `budget` tokens (stem_evict_t).  The
+    numbers are taken when the object is made."""
+    num_seqs: int
+    num_kv_heads: int
+    head_dim: int
+    max_kv_len: int
+    budget: int
+    sink: int = 0
+    recent: int = 0
+    dtype: str = "bf16"
+
+    def __post_init__(self):
+        self._c = _Evict(self.num_seqs, self.num_kv_heads, self.head_dim, _dtype_code(self.dtype), self.max_kv_len,
+                         self.budget, self.sink, self.recent)
+        self._torch = _TORCH_DTYPES[self.dtype]
+
+    @property
+    def c(self):
+        return ctypes.byref(self._c)
+
+    def workspace_bytes(self) -> int:
+        n = lib().stem_evict_workspace_size(self.c)
+        if n == 0:
+            raise StemError(STEM_ERR_INVALID, lib().stem_last_error().decode())
+        return n
+
+
+def evict_workspace(ev: Evict, device="cuda") -> torch.Tensor:
+    return torch.zeros(ev.workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def stem_evict(ev: Evict, src: PagedKV, kv_lens, weights, dst: PagedKV, kv_lens_out=None, weights_out=None, keep=None,
+               ws=None, stream=None):
+    """Keep the first ev.sink, the last ev.recent and the heaviest other tokens of every
+    (sequence, kv-head), ev.budget in all, by weights [num_seqs, Hkv, stride >= max_kv_len];
+    their K/V rows go in order to dst's pages, which must be others than those read.
+    Returns (keep, kv_lens_out): kept positions [num_seqs, Hkv, budget], -1 behind the last,
+    and the new lengths; weights_out [num_seqs, Hkv, stride >= budget] is written if given."""
+    B, Hkv, d, dev, f32 = ev.num_seqs, ev.num_kv_heads, ev.head_dim, weights.device, torch.float32
+    if dev.type != "cuda":
+        raise ValueError("stem_evict takes CUDA tensors")
+    if kv_lens_out is None:
+        kv_lens_out = torch.empty(B, dtype=torch.int32, device=dev)
+    if keep is None:
+        keep = torch.empty((B, Hkv, ev.budget), dtype=torch.int32, device=dev)
+    if ws is None:
+        ws = evict_workspace(ev, dev)
+    _call_on(dev, stream, lib().stem_evict, ev.c, _pages("src", src, B, Hkv, d, ev._torch, dev),
+             _tensor("kv_lens", kv_lens, (B,), torch.int32, dev), _tensor("weights", weights, (B, Hkv, None), f32, dev),
+             weights.shape[-1], _pages("dst", dst, B, Hkv, d, ev._torch, dev),
+             _tensor("kv_lens_out", kv_lens_out, (B,), torch.int32, dev),
+             None if weights_out is None else _tensor("weights_out", weights_out, (B, Hkv, None), f32, dev),
+             0 if weights_out is None else weights_out.shape[-1],
+             _tensor("keep", keep, (B, Hkv, ev.budget), torch.int32, dev), _tensor("ws", ws, (None,), torch.uint8, dev),
+             ws.numel())
+    return keep, kv_lens_out
 
 
 def debug_inject(mode: int) -> None:

@@ -326,6 +326,47 @@ STEM_API stem_status_t stem_decode(const stem_decode_t* dec, const void* q, cons
                                    float* weights_out, int64_t weights_stride, void* out, float* lse, void* ws,
                                    size_t ws_bytes, void* stream);
 
+/* One eviction: every (sequence, kv-head) of a batch cut to `budget` tokens. */
+typedef struct {
+  int num_seqs;                /* B, at most STEM_MAX_DECODE_SEQS */
+  int num_kv_heads;            /* Hkv */
+  int head_dim;                /* d: 64 or 128 (FP8: 128) */
+  stem_dtype_t dtype;          /* storage type of the cache */
+  int max_kv_len;              /* no kv_lens entry exceeds it; 1..STEM_MAX_KV_LEN */
+  int budget;                  /* tokens kept, 1..STEM_MAX_KV_LEN */
+  int sink;                    /* of these, the first tokens of a sequence, kept whatever their weight */
+  int recent;                  /* and the newest ones; sink + recent <= budget */
+} stem_evict_t;
+
+/* Device workspace bytes of stem_evict (0 on a bad problem).  Host only. */
+STEM_API size_t stem_evict_workspace_size(const stem_evict_t* ev);
+
+/*
+ * Eviction from a paged cache by accumulated attention weight (stem_decode's weights_out).
+ * Of a sequence's n = kv_lens[b] tokens every kv-head keeps min(n, budget): all of them where
+ * n <= budget, else the first `sink`, the last `recent`, and of the others those of the
+ * largest weight (equal weights: the lower index; NaN ranks as -inf).  The kept rows of K and
+ * V are copied in ascending order to positions 0, 1, ... of dst's pages; a kv-head's rows
+ * keep their own order, so position i of two heads may hold different tokens (positions are
+ * in the keys already).  src is not changed.
+ * src, dst: the caches and block tables to read and to write (required).  Both may be pages
+ *   of one cache, but no page may be read and written, and no page written twice: that is not
+ *   checked and leaves those pages' contents undefined.
+ * kv_lens: DEVICE int32 [B].  weights: DEVICE float [B, Hkv, weights_stride], stride >= max_kv_len.
+ * kv_lens_out: DEVICE int32 [B], receives min(n, budget); must not be kv_lens.
+ * weights_out: DEVICE float [B, Hkv, weights_out_stride], stride >= budget, receives the kept
+ *   tokens' weights, or NULL; must not overlap weights.
+ * keep: DEVICE int32 [B, Hkv, budget], receives the kept positions, ascending, then -1.
+ * Rows, weights and lengths behind the kept ones are left as they were.  A length outside
+ * [0, max_kv_len] (clamped), a src page outside its cache (slot 0 is read) and a dst page
+ * outside its cache (nothing is written) are reported as STEM_ERR_BOUNDS.
+ * ws: as stem_decode's.
+ */
+STEM_API stem_status_t stem_evict(const stem_evict_t* ev, const stem_paged_kv_t* src, const int32_t* kv_lens,
+                                  const float* weights, int64_t weights_stride, const stem_paged_kv_t* dst,
+                                  int32_t* kv_lens_out, float* weights_out, int64_t weights_out_stride, int32_t* keep,
+                                  void* ws, size_t ws_bytes, void* stream);
+
 /*
  * Synchronise the stream, read and clear the device status word kept in the
  * workspace.  Returns STEM_OK, STEM_ERR_TIMEOUT, STEM_ERR_BOUNDS or STEM_ERR_CUDA.

@@ -139,3 +139,59 @@ def test_oracle_agrees_with_its_own_prefill():
     got, got_lse, w, _, _ = O.decode_rows(q[97:], k, v, 0.3)
     assert np.allclose(got, out[97:]) and np.allclose(got_lse, lse[:, 97:])
     assert np.allclose(w.sum(1), 3 * 2)          # every row's weights add up to one
+
+
+EV = dict(num_seqs=3, num_kv_heads=2, head_dim=128, max_kv_len=1000, budget=100)
+
+
+def evict(L, ev, src=None, dst=None, lens=0x1000, w=0x100000, stride=1000, lens_out=0x2000, w_out=None, stride_out=0,
+          keep=0x1000, ws=0x1000, ws_bytes=256):
+    src = paged() if src is None else src
+    dst = paged(max_pages=2) if dst is None else dst
+    return L.stem_evict(ev.c, ctypes.byref(src) if src else None, lens, w, stride, ctypes.byref(dst) if dst else None,
+                        lens_out, w_out, stride_out, keep, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(num_seqs=0), S.STEM_ERR_INVALID),
+    (dict(num_seqs=1025), S.STEM_ERR_INVALID),
+    (dict(num_kv_heads=0), S.STEM_ERR_INVALID),
+    (dict(num_kv_heads=257), S.STEM_ERR_INVALID),
+    (dict(head_dim=80), S.STEM_ERR_UNSUPPORTED),
+    (dict(head_dim=64, dtype="fp8_e4m3"), S.STEM_ERR_UNSUPPORTED),
+    (dict(max_kv_len=0), S.STEM_ERR_INVALID),
+    (dict(budget=0), S.STEM_ERR_INVALID),
+    (dict(budget=262145), S.STEM_ERR_INVALID),
+    (dict(sink=-1), S.STEM_ERR_INVALID),
+    (dict(recent=-1), S.STEM_ERR_INVALID),
+    (dict(sink=60, recent=41), S.STEM_ERR_INVALID),
+    (dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1), S.STEM_ERR_INVALID),
+])
+def test_evict_refuses_bad_problems(L, change, status):
+    ev = S.Evict(**(EV | change))
+    assert evict(L, ev) == status
+    assert L.stem_evict_workspace_size(ev.c) == 0
+    with pytest.raises(S.StemError):
+        ev.workspace_bytes()
+
+
+def test_evict_refuses_bad_buffers(L):
+    ev = S.Evict(**EV)
+    for kw in (dict(src=False), dict(dst=False), dict(lens=None), dict(w=None), dict(lens_out=None), dict(keep=None),
+               dict(stride=999), dict(lens_out=0x1000), dict(lens_out=0x1008), dict(src=paged(max_pages=15)),
+               dict(dst=paged(max_pages=1)), dict(dst=paged(k=0x1008)), dict(w_out=0x200000, stride_out=99),
+               dict(w_out=0x100010, stride_out=100)):
+        assert evict(L, ev, **kw) == S.STEM_ERR_INVALID, kw
+    assert evict(L, ev, src=paged(page=16)) == S.STEM_ERR_UNSUPPORTED
+    assert evict(L, ev, ws=None) == S.STEM_ERR_WORKSPACE
+    assert evict(L, ev, ws=0x1080) == S.STEM_ERR_WORKSPACE
+    assert evict(L, ev, ws_bytes=255) == S.STEM_ERR_WORKSPACE
+
+
+def test_oracle_eviction_rule_by_hand():
+    w = np.array([0.0, 5.0, 1.0, np.nan, 5.0, 9.0, 0.5])
+    assert O.evict_keep(w, 7, 7, 0, 0).tolist() == list(range(7))
+    assert O.evict_keep(w, 7, 3, 0, 0).tolist() == [1, 4, 5]
+    assert O.evict_keep(w, 7, 2, 0, 0).tolist() == [1, 5]             # the lower of two equal weights
+    assert O.evict_keep(w, 7, 4, 1, 2).tolist() == [0, 1, 5, 6]       # sink, heaviest, recent
+    assert O.evict_keep(w, 7, 6, 0, 0).tolist() == [0, 1, 2, 4, 5, 6]  # NaN goes first
