@@ -48,7 +48,9 @@ struct Cfg {
   static constexpr int TILE = kTile * D * ES;
   static constexpr int STAGE = 2 * TILE;            // K and V
   static constexpr int NST = 96 * 1024 / STAGE;
-  static constexpr int MERGE = 4 * 8 * 64 * 4;      // four warps x 8 rows x 64 columns
+  static constexpr int MROWS = 512 / D;             // rows joined in one round
+  static constexpr int MSTRIDE = D + 8;             // floats: the rows' banks apart
+  static constexpr int MERGE = 4 * MROWS * MSTRIDE * 4;  // of four warps
   static constexpr int OFF_MERGE = NST * STAGE;
   static constexpr int OFF_ML = OFF_MERGE + MERGE;  // float2 [4][16]
   static constexpr int OFF_BAR = OFF_ML + 512;
@@ -62,8 +64,9 @@ struct DecodeParams {
   CUtensorMap tk, tv;        // [slots * 64, Hkv, d]: box (CH, 1, 64)
   DecodeArgs a;
   int rt, prt;               // 16-row tiles of a unit's rows: own, prefix (0: no prefix)
-  int prefix_pages, prefix_tiles;
-  int ctas;
+  int prefix_pages, prefix_span;  // pages of the prefix, its length on the line
+  int gang;                  // CTAs that walk together, each with another kv-head of the same pages
+  int gangs, head_groups;    // ctas / gang, Hkv / gang
 };
 
 __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int b) {
@@ -71,49 +74,98 @@ __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int b) {
 }
 __device__ __forceinline__ int pages_of(int len) { return (len + kTile - 1) / kTile; }
 
+__device__ __forceinline__ int span_of(int pages) { return pages > 0 ? pages + kDecodeUnitCost : 0; }
+
+// Each sequence's first place on the line into cum[0..B] (shared), T threads' worth of
+// sequences at a time; returns the line's length.  `look` sees every length as it came.
+template <int T, typename F>
+__device__ __forceinline__ int line_places(const DecodeParams& p, int* cum, int* sums, F look) {
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int units = p.head_groups * p.rt;
+  int run = p.prefix_span;
+  for (int b0 = 0; b0 < p.a.B; b0 += T) {
+    const int b = b0 + tid;
+    int x = 0;
+    if (b < p.a.B) {
+      const int raw = __ldg(p.a.kv_lens + b);
+      look(raw);
+      x = span_of(pages_of(min(max(raw, 0), p.a.max_kv_len))) * units;
+    }
+    int inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (b0 > 0) __syncthreads();
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    int before = run, sum = 0;
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w) {
+      const int v = sums[w];
+      before += w < warp ? v : 0;
+      sum += v;
+    }
+    if (b < p.a.B) cum[b] = before + inc - x;
+    run += sum;
+  }
+  if (tid == 0) cum[p.a.B] = run;
+  __syncthreads();
+  return run;
+}
+
 // One CTA's share of one unit.
 struct Seg {
   bool own;
-  int b, kvh, rtile, unit;
+  int b, kvh, rtile;
+  int unit;            // index on the line of one gang member
   int p0, p1, pages, len;
 };
 
-// Walks the units of the tiles [t, end) in line order.
+// Walks the units of [t, end) in line order: the prefix's (head group, row tile), then
+// sequence after sequence (head group, row tile); a gang's member `rank` takes the head
+// group's head of that number.
 struct Walk {
-  int t, end, b, base, len;
+  int t, end, b, base, len, rank;
   __device__ __forceinline__ bool next(const DecodeParams& p, Seg* s) {
-    if (t >= end) return false;
-    if (t < p.prefix_tiles) {
-      const int u = t / p.prefix_pages;
-      s->own = false;
-      s->unit = u;
-      s->kvh = u / p.prt;
-      s->rtile = u % p.prt;
-      s->b = 0;
-      s->pages = p.prefix_pages;
-      s->len = p.a.prefix_len;
-      s->p0 = t - u * p.prefix_pages;
-    } else {
-      const int per_page = p.a.Hkv * p.rt;
-      int pages = pages_of(len);
-      while (t >= base + pages * per_page) {
-        base += pages * per_page;
-        len = clamp_len(p.a, ++b);
-        pages = pages_of(len);
+    while (t < end) {
+      int at;  // place inside the unit, the empty tiles first
+      if (t < p.prefix_span) {
+        const int span = p.prefix_pages + kDecodeUnitCost, u = t / span;
+        s->own = false;
+        s->unit = u;
+        s->kvh = u / p.prt * p.gang + rank;
+        s->rtile = u % p.prt;
+        s->b = 0;
+        s->pages = p.prefix_pages;
+        s->len = p.a.prefix_len;
+        at = t - u * span;
+      } else {
+        const int units = p.head_groups * p.rt;
+        int span = span_of(pages_of(len));
+        while (t >= base + span * units) {
+          base += span * units;
+          len = clamp_len(p.a, ++b);
+          span = span_of(pages_of(len));
+        }
+        const int u = (t - base) / span;
+        s->own = true;
+        s->unit = p.head_groups * (p.prt + b * p.rt) + u;
+        s->kvh = u / p.rt * p.gang + rank;
+        s->rtile = u % p.rt;
+        s->b = b;
+        s->pages = span - kDecodeUnitCost;
+        s->len = len;
+        at = t - base - u * span;
       }
-      const int u = (t - base) / pages;
-      s->own = true;
-      s->unit = p.a.Hkv * (p.prt + b * p.rt) + u;
-      s->kvh = u / p.rt;
-      s->rtile = u % p.rt;
-      s->b = b;
-      s->pages = pages;
-      s->len = len;
-      s->p0 = t - base - u * pages;
+      const int stop = min(s->pages + kDecodeUnitCost, at + (end - t));
+      t += stop - at;
+      s->p0 = max(0, at - kDecodeUnitCost);
+      s->p1 = stop - kDecodeUnitCost;
+      if (s->p1 > s->p0) return true;
     }
-    s->p1 = min(s->pages, s->p0 + (end - t));
-    t += s->p1 - s->p0;
-    return true;
+    return false;
   }
 };
 
@@ -153,8 +205,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // 16-bit masks of a fragment register that holds tokens j and j + 1: the halves whose
 // token is at or behind `limit` become zero (masked V rows may hold NaN).
@@ -181,7 +231,6 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const unsigned all = 0xffffffffu;
 
-  pdl_trigger();
   if (tid == 0) {
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(full(s), 1);
@@ -189,61 +238,32 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     }
     *abort_flag = 0;
     plan[0] = 0;
-    plan[1] = p.prefix_tiles;
+    plan[1] = p.prefix_span;
     mbar_fence_init();
+    tma_prefetch_map(&p.tk);
+    tma_prefetch_map(&p.tv);
   }
-  // first tile of every sequence (exclusive sums of the unit tiles), 160 sequences at a time
+  pdl_wait();     // nothing of the caller's, nor the workspace, is touched before
+  pdl_trigger();  // not earlier: decode_finish reads the lengths before its own wait
   int* cum = reinterpret_cast<int*>(merge);
-  int run = p.prefix_tiles;
-  const int per_page = a.Hkv * p.rt;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    int x = 0;
-    if (b < a.B) {
-      const int raw = __ldg(a.kv_lens + b);
-      if (blockIdx.x == 0 && (raw < 0 || raw > a.max_kv_len)) atomicOr(a.status, kStatusBounds);
-      x = pages_of(min(max(raw, 0), a.max_kv_len)) * per_page;
-    }
-    int inc = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(all, inc, o);
-      if (lane >= o) inc += y;
-    }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = inc;
-    __syncthreads();
-    int before = run, sum = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += warp_sums[w];
-      sum += warp_sums[w];
-    }
-    if (b < a.B) cum[b] = before + inc - x;
-    run += sum;
-  }
-  if (tid == 0) cum[a.B] = run;
-  __syncthreads();
-  const int per = (run + p.ctas - 1) / p.ctas;
-  const int t0 = min(run, static_cast<int>(blockIdx.x) * per), t1 = min(run, t0 + per);
+  const int run = line_places<kThreads>(p, cum, warp_sums, [&](int raw) {
+    if (blockIdx.x == 0 && (raw < 0 || raw > a.max_kv_len)) atomicOr(a.status, kStatusBounds);
+  });
+  const int gang_no = static_cast<int>(blockIdx.x) / p.gang, rank = static_cast<int>(blockIdx.x) % p.gang;
+  const int per = (run + p.gangs - 1) / p.gangs;
+  const int t0 = min(run, gang_no * per), t1 = min(run, t0 + per);
   for (int b = tid; b < a.B; b += kThreads) {
     if (cum[b] <= t0 && t0 < cum[b + 1]) {
       plan[0] = b;
       plan[1] = cum[b];
     }
   }
-  if (blockIdx.x == 0)
-    for (int b = tid; b <= a.B; b += kThreads) a.cum[b] = cum[b];
   __syncthreads();
-  Walk walk{t0, t1, plan[0], plan[1], clamp_len(a, plan[0])};
+  Walk walk{t0, t1, plan[0], plan[1], clamp_len(a, plan[0]), rank};
   Seg sg;
 
   if (warp == 4) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      tma_prefetch_map(&p.tk);
-      tma_prefetch_map(&p.tv);
-    }
     uint32_t it = 0;
     bool alive = true;
     while (alive && walk.next(p, &sg)) {
@@ -347,11 +367,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         const uint32_t kt = sring + st * C::STAGE, vt = kt + C::TILE;
         const int s0 = pg * kTile + warp * 16;     // this warp's first token
         // S = Q K^T for 16 tokens
-        float s[2][4];
+        // (two accumulators each, for half the chain of dependent products)
+        float s[2][4], s_odd[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[j][e] = s_odd[j][e] = 0.f;
         if (FP8) {
 #pragma unroll
           for (int k = 0; k < D / 16; k += 2) {
@@ -361,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                mma16816<true>(s[j], qf[k + kk], e4m3x2_to_h2(r[2 * kk + j] & 0xFFFFu), e4m3x2_to_h2(r[2 * kk + j] >> 16));
+                mma16816<true>(kk ? s_odd[j] : s[j], qf[k + kk], e4m3x2_to_h2(r[2 * kk + j] & 0xFFFFu), e4m3x2_to_h2(r[2 * kk + j] >> 16));
           }
         } else {
 #pragma unroll
@@ -369,14 +390,14 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
             const int c = 2 * k + k_sub;
             uint32_t r[4];
             ldsm4(r, kt + (c >> 3) * C::CHUNK + k_row + (((c & 7) ^ sw) << 4));
-            mma16816<false>(s[0], qf[k], r[0], r[1]);
-            mma16816<false>(s[1], qf[k], r[2], r[3]);
+            mma16816<false>(k & 1 ? s_odd[0] : s[0], qf[k], r[0], r[1]);
+            mma16816<false>(k & 1 ? s_odd[1] : s[1], qf[k], r[2], r[3]);
           }
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[j][e] *= a.scale_log2;
+          for (int e = 0; e < 4; ++e) s[j][e] = (s[j][e] + s_odd[j][e]) * a.scale_log2;
         const bool edge = s0 + 16 > lim_lo;
         if (edge) {
 #pragma unroll
@@ -503,88 +524,92 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       ml[warp * 16 + r0 + 8] = make_float2(m1, l1);
     }
     const bool direct = sg.own && sg.p0 == 0 && sg.p1 == sg.pages && p.prt == 0;
-    const long long slot = static_cast<long long>(blockIdx.x) + sg.unit;
+    const long long slot = static_cast<long long>(gang_no + sg.unit) * p.gang + rank;
+    // rounds of 4 rows x 128 columns (d 64: 8 rows x 64): few rows, few barriers
+    constexpr int RPR = C::MROWS;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (8 * half >= nrows) break;
+    for (int round = 0; round < kDecodeRows / RPR; ++round) {
+      if (round * RPR >= nrows) break;
+      const int half = round * RPR / 8;
+      if (r0 / RPR == round % (8 / RPR)) {
+        float* mine = merge + (warp * RPR + r0 % RPR) * C::MSTRIDE;
 #pragma unroll
-      for (int ch = 0; ch < D / 64; ++ch) {
-        float* mine = merge + (warp * 8 + r0) * 64;
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const int x = ch * 8 + i;
+        for (int x = 0; x < D / 8; x += 2) {
           if (FP8) {
-            *reinterpret_cast<float4*>(mine + i * 8 + qd * 4) = make_float4(
+            *reinterpret_cast<float4*>(mine + x * 8 + qd * 4) = make_float4(
                 acc[x][2 * half], acc[x + 1][2 * half], acc[x][2 * half + 1], acc[x + 1][2 * half + 1]);
           } else {
-            *reinterpret_cast<float2*>(mine + i * 8 + qd * 2) = make_float2(acc[x][2 * half], acc[x][2 * half + 1]);
-            *reinterpret_cast<float2*>(mine + i * 8 + 8 + qd * 2) =
+            *reinterpret_cast<float2*>(mine + x * 8 + qd * 2) = make_float2(acc[x][2 * half], acc[x][2 * half + 1]);
+            *reinterpret_cast<float2*>(mine + x * 8 + 8 + qd * 2) =
                 make_float2(acc[x + 1][2 * half], acc[x + 1][2 * half + 1]);
           }
         }
-        consumer_sync();
-        const int rr = tid / 16, r = half * 8 + rr, col = (tid % 16) * 4;  // 8 rows x 16 groups of 4 columns
-        if (r < nrows) {
-          float M = -INFINITY;
-          float2 v[4];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            v[w] = ml[w * 16 + r];
-            M = fmaxf(M, v[w].x);
-          }
-          float L = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const float f = v[w].x == -INFINITY ? 0.f : ex2_approx(v[w].x - M);
-            const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + rr) * 64 + col);
-            L += f * v[w].y;
-            o.x += f * x.x;
-            o.y += f * x.y;
-            o.z += f * x.z;
-            o.w += f * x.w;
-          }
-          const bool lead = ch == 0 && col == 0;
-          if (direct) {
-            const int g = row_base + r;
-            const long long tok = g / G;
-            const int h = sg.kvh * G + g % G;
-            const float inv = M == -INFINITY && L == 0.f ? 0.f : a.v_scale / L;  // nothing seen: o = 0
-            *reinterpret_cast<uint2*>(static_cast<unsigned char*>(a.out) + ((tok * a.Hq + h) * D + ch * 64 + col) * 2) =
-                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-            if (a.lse != nullptr && lead)
-              a.lse[static_cast<long long>(h) * a.B * a.n + tok] =
-                  L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
-          } else {
-            *reinterpret_cast<float4*>(a.part_o + (slot * a.part_rows + r) * D + ch * 64 + col) = o;
-          }
-          if (lead && (!direct || SCORES)) a.part_ml[slot * kDecodeRows + r] = make_float2(M, L);
-        }
-        consumer_sync();
       }
+      consumer_sync();
+      const int rr = tid / (D / 4), r = round * RPR + rr, col = tid % (D / 4) * 4;  // RPR rows x groups of 4 columns
+      if (r < nrows) {
+        float M = -INFINITY;
+        float2 v[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          v[w] = ml[w * 16 + r];
+          M = fmaxf(M, v[w].x);
+        }
+        float L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float f = v[w].x == -INFINITY ? 0.f : ex2_approx(v[w].x - M);
+          const float4 x = *reinterpret_cast<const float4*>(merge + (w * RPR + rr) * C::MSTRIDE + col);
+          L += f * v[w].y;
+          o.x += f * x.x;
+          o.y += f * x.y;
+          o.z += f * x.z;
+          o.w += f * x.w;
+        }
+        if (direct) {
+          const int g = row_base + r;
+          const long long tok = g / G;
+          const int h = sg.kvh * G + g % G;
+          const float inv = M == -INFINITY && L == 0.f ? 0.f : a.v_scale / L;  // nothing seen: o = 0
+          *reinterpret_cast<uint2*>(static_cast<unsigned char*>(a.out) + ((tok * a.Hq + h) * D + col) * 2) =
+              make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+          if (a.lse != nullptr && col == 0)
+            a.lse[static_cast<long long>(h) * a.B * a.n + tok] =
+                L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + (slot * a.part_rows + r) * D + col) = o;
+        }
+        if (col == 0 && (!direct || SCORES)) a.part_ml[slot * kDecodeRows + r] = make_float2(M, L);
+      }
+      consumer_sync();
     }
   }
 }
 
-// The partials of one row's unit: CTAs c0..c1 share tiles [u0, u0 + pages) of the line.
+// The partials of one unit: slots `slot`, `slot + step`, ...
 struct Pieces {
-  long long slot;    // first slot; the following ones are adjacent
-  int n;
+  long long slot;
+  int n, step;
 };
-__device__ __forceinline__ Pieces pieces_of(int first_tile, int pages, int unit, int per) {
-  if (pages == 0) return Pieces{0, 0};
-  const int c0 = first_tile / per, c1 = (first_tile + pages - 1) / per;
-  return Pieces{static_cast<long long>(c0) + unit, c1 - c0 + 1};
+__device__ __forceinline__ Pieces pieces_of(const DecodeParams& p, int start, int pages, int unit, int rank, int per) {
+  if (pages == 0) return Pieces{0, 0, 1};
+  const int c0 = (start + kDecodeUnitCost) / per, c1 = (start + kDecodeUnitCost + pages - 1) / per;
+  return Pieces{static_cast<long long>(c0 + unit) * p.gang + rank, c1 - c0 + 1, p.gang};
 }
 __device__ __forceinline__ Pieces own_pieces(const DecodeParams& p, int per, int b, int base, int pages, int kvh,
                                              int rtile) {
-  const int u = kvh * p.rt + rtile;
-  return pieces_of(base + u * pages, pages, p.a.Hkv * (p.prt + b * p.rt) + u, per);
+  const int u = kvh / p.gang * p.rt + rtile;
+  return pieces_of(p, base + u * span_of(pages), pages, p.head_groups * (p.prt + b * p.rt) + u, kvh % p.gang, per);
 }
 __device__ __forceinline__ Pieces prefix_pieces(const DecodeParams& p, int per, int kvh, int row) {
-  if (p.prt == 0) return Pieces{0, 0};
-  const int u = kvh * p.prt + row / kDecodeRows;
-  return pieces_of(u * p.prefix_pages, p.prefix_pages, u, per);
+  if (p.prt == 0) return Pieces{0, 0, 1};
+  const int u = kvh / p.gang * p.prt + row / kDecodeRows;
+  return pieces_of(p, u * (p.prefix_pages + kDecodeUnitCost), p.prefix_pages, u, kvh % p.gang, per);
+}
+// Pages of a sequence from its length on the line.
+__device__ __forceinline__ int pages_on_line(const DecodeParams& p, int length) {
+  return length > 0 ? length / (p.head_groups * p.rt) - kDecodeUnitCost : 0;
 }
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -598,61 +623,129 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
+// A row's partials, the own ones first: statistics of number i.
+struct RowPieces {
+  Pieces own, pre;
+  int own_row, pre_row;
+  __device__ __forceinline__ int count() const { return own.n + pre.n; }
+  __device__ __forceinline__ long long slot(int i) const {
+    return i < own.n ? own.slot + static_cast<long long>(i) * own.step
+                     : pre.slot + static_cast<long long>(i - own.n) * pre.step;
+  }
+  __device__ __forceinline__ int row(int i) const { return i < own.n ? own_row : pre_row; }
+};
+__device__ __forceinline__ RowPieces row_pieces(const DecodeParams& p, int per, int b, int base, int pages, int kvh,
+                                                int rr) {
+  const int pr = b * p.a.n * p.a.G + rr;
+  return RowPieces{own_pieces(p, per, b, base, pages, kvh, rr / kDecodeRows), prefix_pieces(p, per, kvh, pr),
+                   rr % kDecodeRows, pr % kDecodeRows};
+}
+
+// 2^(m - M), for a partial whose scores were all -inf 0 (and 1 where its sum is NaN: the
+// NaN has to arrive).
+__device__ __forceinline__ float piece_factor(float2 v, float M) {
+  return v.x == -INFINITY ? (v.y == 0.f ? 0.f : 1.f) : ex2_approx(v.x - M);
+}
+
 // Maximum and sum over a row's partials (all lanes get both).
-__device__ __forceinline__ float2 row_stats(const DecodeArgs& a, Pieces own, int own_row, Pieces pre, int pre_row) {
-  const int lane = threadIdx.x % 32;
-  float M = -INFINITY;
-  for (int i = lane; i < own.n; i += 32) M = fmaxf(M, a.part_ml[(own.slot + i) * kDecodeRows + own_row].x);
-  for (int i = lane; i < pre.n; i += 32) M = fmaxf(M, a.part_ml[(pre.slot + i) * kDecodeRows + pre_row].x);
+__device__ __forceinline__ float2 row_stats(const DecodeArgs& a, const RowPieces& q) {
+  const int lane = threadIdx.x % 32, n = q.count();
+  float2 v = make_float2(-INFINITY, 0.f);
+  if (lane < n) v = a.part_ml[q.slot(lane) * kDecodeRows + q.row(lane)];
+  float M = v.x;
+  for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, a.part_ml[q.slot(i) * kDecodeRows + q.row(i)].x);
   M = warp_max(M);
-  float L = 0.f;
-  auto add = [&](long long slot, int row) {
-    const float2 v = a.part_ml[slot * kDecodeRows + row];
-    if (v.x != -INFINITY) L += ex2_approx(v.x - M) * v.y;
-    else L += v.y;  // zero, or the NaN of a row whose scores are all NaN
-  };
-  for (int i = lane; i < own.n; i += 32) add(own.slot + i, own_row);
-  for (int i = lane; i < pre.n; i += 32) add(pre.slot + i, pre_row);
+  float L = piece_factor(v, M) * v.y;
+  for (int i = lane + 32; i < n; i += 32) {
+    v = a.part_ml[q.slot(i) * kDecodeRows + q.row(i)];
+    L += piece_factor(v, M) * v.y;
+  }
   return make_float2(M, warp_sum(L));
 }
 
-// Joins the partials of rows whose keys fell to several CTAs (blocks below row_blocks, one
-// warp per row) and adds up the softmax weights (the other blocks, from the stored scores).
-template <int D, bool SCORES>
+template <int E>
+__device__ __forceinline__ void load_share(float (&x)[E], const float* src) {
+  if constexpr (E == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(src);
+    x[0] = v.x;
+    x[1] = v.y;
+    x[2] = v.z;
+    x[3] = v.w;
+  } else {
+    const float2 v = *reinterpret_cast<const float2*>(src);
+    x[0] = v.x;
+    x[1] = v.y;
+  }
+}
+
+// Joins the partials of rows whose keys fell to several CTAs (blocks below row_blocks, WPR
+// warps per row) and adds up the softmax weights (the other blocks, from the stored scores).
+// What follows pdl_wait is latency, so where each row's partials lie is worked out before
+// it, from the lengths (decode_kernel triggers this launch after its own wait, when all that
+// came before it in the stream is complete), and all loads after it are independent.
+template <int D, bool SCORES, int WPR>
 __global__ void __launch_bounds__(kFinishThreads) decode_finish(const __grid_constant__ DecodeParams p, int row_blocks) {
   const DecodeArgs& a = p.a;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, G = a.G, R = a.n * G;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, G = a.G, R = a.n * G;
+  constexpr int E = D / 32, RPB = kFinishThreads / 32 / WPR;  // columns of a lane, rows of a block
+  constexpr int PF = WPR > 1 ? 8 : 4;                         // partials a warp loads at once
+  __shared__ int cum[STEM_MAX_DECODE_SEQS + 1];
+  __shared__ int sums[kFinishThreads / 32];
   __shared__ float lse2[256];
-  __shared__ int where[2];
-  pdl_wait();
-  const int total = a.cum[a.B];
-  const int per = max(1, (total + p.ctas - 1) / p.ctas);
+  __shared__ float shares[WPR > 1 ? kFinishThreads * E : 1];
+  __shared__ int where;
+  pdl_trigger();
+  const int total = line_places<kFinishThreads>(p, cum, sums, [](int) {});
+  const int per = max(1, (total + p.gangs - 1) / p.gangs);
 
   if (static_cast<int>(blockIdx.x) < row_blocks) {
-    const long long row = static_cast<long long>(blockIdx.x) * (kFinishThreads / 32) + warp;  // token-major, then head
-    if (row >= static_cast<long long>(a.B) * a.n * a.Hq) return;
+    const long long row = static_cast<long long>(blockIdx.x) * RPB + warp / WPR;  // token-major, then head
+    if (row >= static_cast<long long>(a.B) * a.n * a.Hq) return;                  // never with WPR = 8 (one row)
     const int tok = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
-    const int b = tok / a.n, kvh = h / G, rr = (tok % a.n) * G + h % G, pr = b * R + rr;
-    const int base = a.cum[b], pages = (a.cum[b + 1] - base) / (a.Hkv * p.rt);
-    const Pieces own = own_pieces(p, per, b, base, pages, kvh, rr / kDecodeRows);
-    const Pieces pre = prefix_pieces(p, per, kvh, pr);
-    if (p.prt == 0 && own.n == 1) return;  // written by the CTA that saw all of it
-    const float2 st = row_stats(a, own, rr % kDecodeRows, pre, pr % kDecodeRows);
-    constexpr int E = D / 32;
+    const int b = tok / a.n, kvh = h / G, rr = (tok % a.n) * G + h % G;
+    const int base = cum[b], pages = pages_on_line(p, cum[b + 1] - base);
+    const RowPieces q = row_pieces(p, per, b, base, pages, kvh, rr);
+    const int n = q.count(), w = warp % WPR;
+    if (p.prt == 0 && n == 1) return;  // written by the CTA that saw all of it
+    pdl_wait();
+    auto share_of = [&](int i) { return a.part_o + (q.slot(i) * a.part_rows + q.row(i)) * D + lane * E; };
+    auto stats_of = [&](int i) { return a.part_ml[q.slot(i) * kDecodeRows + q.row(i)]; };
+    float x[PF][E];
+    float2 v[PF];
+#pragma unroll
+    for (int k = 0; k < PF; ++k)
+      if (w + WPR * k < n) {
+        load_share(x[k], share_of(w + WPR * k));
+        v[k] = stats_of(w + WPR * k);
+      }
+    const float2 st = row_stats(a, q);
     float o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    auto add = [&](long long slot, int r) {
-      const float2 v = a.part_ml[slot * kDecodeRows + r];
-      const float f = v.x == -INFINITY ? (v.y == 0.f ? 0.f : 1.f) : ex2_approx(v.x - st.x);
-      const float* src = a.part_o + (slot * a.part_rows + r) * D + lane * E;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += f * src[e];
-    };
+    for (int k = 0; k < PF; ++k)
+      if (w + WPR * k < n) {
+        const float f = piece_factor(v[k], st.x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += f * x[k][e];
+      }
 #pragma unroll 4
-    for (int i = 0; i < own.n; ++i) add(own.slot + i, rr % kDecodeRows);
-#pragma unroll 4
-    for (int i = 0; i < pre.n; ++i) add(pre.slot + i, pr % kDecodeRows);
+    for (int i = w + WPR * PF; i < n; i += WPR) {
+      load_share(x[0], share_of(i));
+      const float f = piece_factor(stats_of(i), st.x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += f * x[0][e];
+    }
+    if constexpr (WPR > 1) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) shares[tid * E + e] = o[e];
+      __syncthreads();
+      if (w != 0) return;
+#pragma unroll
+      for (int y = 1; y < WPR; ++y)
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += shares[(tid + 32 * y) * E + e];
+    }
     const float inv = st.x == -INFINITY && st.y == 0.f ? 0.f : a.v_scale / st.y;
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.out) +
                                                 ((static_cast<long long>(tok) * a.Hq + h) * D + lane * E) * 2);
@@ -665,75 +758,78 @@ __global__ void __launch_bounds__(kFinishThreads) decode_finish(const __grid_con
   }
 
   if constexpr (SCORES) {
-    // An equal share of the own pages of all (sequence, kv-head) pairs, in line order.
-    const int nb = gridDim.x - row_blocks, c = blockIdx.x - row_blocks;
-    const int lines = (total - p.prefix_tiles) / p.rt;
-    const int share = (lines + nb - 1) / nb;
-    int t = min(lines, c * share);
-    const int end = min(lines, t + share);
-    while (t < end) {
-      if (threadIdx.x == 0) where[0] = -1;
-      __syncthreads();
-      for (int b = threadIdx.x; b < a.B; b += kFinishThreads) {
-        const int lo = (a.cum[b] - p.prefix_tiles) / p.rt, hi = (a.cum[b + 1] - p.prefix_tiles) / p.rt;
-        if (lo <= t && t < hi) where[0] = b;
+    // Chunks of 1024 tokens (4 per thread) of all (sequence, kv-head) pairs, dealt round robin.
+    __shared__ int chunk_cum[STEM_MAX_DECODE_SEQS + 1];
+    constexpr int kChunk = kFinishThreads * 4 / kTile;  // pages
+    if (warp == 0) {
+      int run = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int b = b0 + lane;
+        const int y = b < a.B ? (pages_on_line(p, cum[b + 1] - cum[b]) + kChunk - 1) / kChunk * a.Hkv : 0;
+        int inc = y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int z = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += z;
+        }
+        if (b < a.B) chunk_cum[b] = run + inc - y;
+        run += __shfl_sync(0xffffffffu, inc, 31);
       }
+      if (lane == 0) chunk_cum[a.B] = run;
+    }
+    __syncthreads();
+    const int chunks = chunk_cum[a.B], nb = gridDim.x - row_blocks;
+    bool waited = false;
+    for (int c = blockIdx.x - row_blocks; c < chunks; c += nb) {
+      for (int b = tid; b < a.B; b += kFinishThreads)
+        if (chunk_cum[b] <= c && c < chunk_cum[b + 1]) where = b;
       __syncthreads();
-      const int b = where[0];
-      const int base = a.cum[b], pages = (a.cum[b + 1] - base) / (a.Hkv * p.rt);
-      const int off = t - (base - p.prefix_tiles) / p.rt, kvh = off / pages, p0 = off % pages;
-      const int p1 = min(pages, p0 + (end - t)), len = clamp_len(a, b);
+      const int b = where;
+      const int base = cum[b], pages = pages_on_line(p, cum[b + 1] - base);
+      const int off = c - chunk_cum[b], each = (pages + kChunk - 1) / kChunk, kvh = off / each;
+      const int len = clamp_len(a, b), j = (off % each) * (kFinishThreads * 4) + tid * 4;
       const long long unit = static_cast<long long>(b) * a.Hkv + kvh;
       const float* win = a.weights_in ? a.weights_in + unit * a.weights_stride : nullptr;
       float* wout = a.weights_out + unit * a.weights_stride;
+      if (!waited) pdl_wait();
+      waited = true;
+      float sum[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = win && j + e < len ? win[j + e] : 0.f;
+      float add[4] = {0.f, 0.f, 0.f, 0.f};
       for (int r0 = 0; r0 < R; r0 += 256) {
         const int nr = min(256, R - r0);
+        const float* sc = a.scores + (unit * R + r0) * a.score_stride + j;
+        float4 x[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (r < nr && j < len) x[r] = *reinterpret_cast<const float4*>(sc + r * a.score_stride);
         for (int r = warp; r < nr; r += kFinishThreads / 32) {
-          const int rr = r0 + r, pr = b * R + rr;
-          const float2 st = row_stats(a, own_pieces(p, per, b, base, pages, kvh, rr / kDecodeRows), rr % kDecodeRows,
-                                      prefix_pieces(p, per, kvh, pr), pr % kDecodeRows);
+          const float2 st = row_stats(a, row_pieces(p, per, b, base, pages, kvh, r0 + r));
           // a row that sees nothing adds exp2(-inf - inf) = 0
           if (lane == 0) lse2[r] = st.y == 0.f ? INFINITY : st.x + log2f(st.y);
         }
         __syncthreads();
-        const float* sc = a.scores + (unit * R + r0) * a.score_stride;
-        for (int j = p0 * kTile + threadIdx.x * 4; j < min(len, p1 * kTile); j += kFinishThreads * 4) {
-          float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-          for (int r = 0; r < nr; ++r) {
-            const float4 x = *reinterpret_cast<const float4*>(sc + r * a.score_stride + j);
-            w[0] += ex2_approx(x.x - lse2[r]);
-            w[1] += ex2_approx(x.y - lse2[r]);
-            w[2] += ex2_approx(x.z - lse2[r]);
-            w[3] += ex2_approx(x.w - lse2[r]);
-          }
+        auto take = [&](const float4& y, float l) {
+          add[0] += ex2_approx(y.x - l);
+          add[1] += ex2_approx(y.y - l);
+          add[2] += ex2_approx(y.z - l);
+          add[3] += ex2_approx(y.w - l);
+        };
+        if (j < len) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (j + e < len) {
-              const float was = r0 > 0 ? wout[j + e] : (win ? win[j + e] : 0.f);
-              wout[j + e] = was + w[e];
-            }
+          for (int r = 0; r < 4; ++r)
+            if (r < nr) take(x[r], lse2[r]);
+#pragma unroll 4
+          for (int r = 4; r < nr; ++r) take(*reinterpret_cast<const float4*>(sc + r * a.score_stride), lse2[r]);
         }
         __syncthreads();
       }
-      t += p1 - p0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < len) wout[j + e] = sum[e] + add[e];
     }
   }
-}
-
-template <typename K, typename... A>
-cudaError_t launch_dependent(K kern, int grid, int threads, size_t smem, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <int D, bool FP8, bool SCORES>
@@ -741,14 +837,21 @@ cudaError_t run(const DecodeParams& prm, cudaStream_t st) {
   using C = Cfg<D, FP8>;
   cudaError_t e = set_smem_once<decode_kernel<D, FP8, SCORES>>(C::SMEM);
   if (e != cudaSuccess) return e;
-  decode_kernel<D, FP8, SCORES><<<prm.ctas, kThreads, C::SMEM, st>>>(prm);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_dependent(decode_kernel<D, FP8, SCORES>, prm.gangs * prm.gang, kThreads, C::SMEM, 1, st, prm);
+  if (e != cudaSuccess) return e;
   const DecodeArgs& a = prm.a;
   const long long rows = static_cast<long long>(a.B) * a.n * a.Hq;
-  const int row_blocks = static_cast<int>((rows + kFinishThreads / 32 - 1) / (kFinishThreads / 32));
-  const long long pages = static_cast<long long>(a.B) * a.Hkv * ((a.max_kv_len + kTile - 1) / kTile);
-  const int weight_blocks = SCORES ? static_cast<int>(pages < 2 * kDecodeCtas ? pages : 2 * kDecodeCtas) : 0;
-  return launch_dependent(decode_finish<D, SCORES>, row_blocks + weight_blocks, kFinishThreads, 0, st, prm, row_blocks);
+  const long long chunks =
+      static_cast<long long>(a.B) * a.Hkv * ((a.max_kv_len + kFinishThreads * 4 - 1) / (kFinishThreads * 4));
+  const int weight_blocks = SCORES ? static_cast<int>(chunks < 3 * kDecodeCtas ? chunks : 3 * kDecodeCtas) : 0;
+  // Few rows have many partials each (their tiles are spread over all CTAs): a block per row
+  // then, else a warp per row.
+  if (rows <= kDecodeCtas)
+    return launch_dependent(decode_finish<D, SCORES, 8>, static_cast<int>(rows) + weight_blocks, kFinishThreads, 0, 1,
+                            st, prm, static_cast<int>(rows));
+  const int row_blocks = static_cast<int>((rows + 7) / 8);
+  return launch_dependent(decode_finish<D, SCORES, 1>, row_blocks + weight_blocks, kFinishThreads, 0, 1, st, prm,
+                          row_blocks);
 }
 
 }  // namespace
@@ -765,15 +868,23 @@ cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st) {
   prm.rt = (R + kDecodeRows - 1) / kDecodeRows;
   prm.prt = a.prefix_len > 0 ? (a.B * R + kDecodeRows - 1) / kDecodeRows : 0;
   prm.prefix_pages = (a.prefix_len + kTile - 1) / kTile;
-  prm.prefix_tiles = a.Hkv * prm.prt * prm.prefix_pages;
+  // The gang: kv-heads are neighbours in memory (a page of one head is 64 pieces of 128 or
+  // 256 bytes), so CTAs that read the same pages at the same time, a head each, read whole
+  // DRAM rows.
+  prm.gang = 1;
+  for (int g = 2; g <= 8; ++g)
+    if (a.Hkv % g == 0) prm.gang = g;
+  prm.head_groups = a.Hkv / prm.gang;
+  prm.prefix_span = prm.prt > 0 ? prm.head_groups * prm.prt * (prm.prefix_pages + kDecodeUnitCost) : 0;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const long long bound =
-      prm.prefix_tiles + static_cast<long long>(a.B) * a.Hkv * prm.rt * ((a.max_kv_len + kTile - 1) / kTile);
-  prm.ctas = 2 * sms < kDecodeCtas ? 2 * sms : kDecodeCtas;
-  if (bound < prm.ctas) prm.ctas = static_cast<int>(bound);
+  const long long bound = static_cast<long long>(prm.head_groups) *
+                          (prm.prt * prm.prefix_pages +
+                           static_cast<long long>(a.B) * prm.rt * ((a.max_kv_len + kTile - 1) / kTile));
+  prm.gangs = (2 * sms < kDecodeCtas ? 2 * sms : kDecodeCtas) / prm.gang;
+  if (bound < prm.gangs) prm.gangs = static_cast<int>(bound);
   const bool scores = a.scores != nullptr;
   if (fp8) return scores ? run<128, true, true>(prm, st) : run<128, true, false>(prm, st);
   if (a.d == 128) return scores ? run<128, false, true>(prm, st) : run<128, false, false>(prm, st);

@@ -70,8 +70,8 @@ stem_status_t check_decode(const stem_decode_t* de) {
   const long long R = static_cast<long long>(de->q_len) * (de->num_q_heads / de->num_kv_heads);
   const long long pages = (de->max_kv_len + STEM_PAGE_SIZE - 1) / STEM_PAGE_SIZE;
   const long long ppages = (de->prefix_len + STEM_PAGE_SIZE - 1) / STEM_PAGE_SIZE;
-  const long long own = de->num_kv_heads * de->num_seqs * ((R + kDecodeRows - 1) / kDecodeRows) * pages;
-  const long long pre = de->num_kv_heads * ((de->num_seqs * R + kDecodeRows - 1) / kDecodeRows) * ppages;
+  const long long own = de->num_kv_heads * de->num_seqs * ((R + kDecodeRows - 1) / kDecodeRows) * (pages + kDecodeUnitCost);
+  const long long pre = de->num_kv_heads * ((de->num_seqs * R + kDecodeRows - 1) / kDecodeRows) * (ppages + kDecodeUnitCost);
   if (own + pre > (1ll << 30))
     return set_last_error(STEM_ERR_UNSUPPORTED, "batch x heads x pages of %lld tiles is too large", own + pre);
   return STEM_OK;
@@ -99,8 +99,6 @@ DecodeWs layout(const stem_decode_t* de) {
   const size_t most = prt > 0 ? B * R : R;
   w.part_rows = static_cast<int>(most < kDecodeRows ? most : kDecodeRows);
   size_t o = 256;
-  w.cum = o;
-  o = align256(o + (B + 1) * 4);
   w.part_ml = o;
   o = align256(o + slots * kDecodeRows * sizeof(float2));
   w.part_o = o;
@@ -191,7 +189,6 @@ stem_status_t stem_decode(const stem_decode_t* dec, const void* q, const stem_pa
   a.out = out;
   a.lse = lse;
   a.status = at<uint32_t>(ws, w.status);
-  a.cum = at<int32_t>(ws, w.cum);
   a.part_ml = at<float2>(ws, w.part_ml);
   a.part_o = at<float>(ws, w.part_o);
   a.scores = dec->collect_weights ? at<float>(ws, w.scores) : nullptr;

@@ -5,15 +5,14 @@
 // pages.  Two launches:
 //   evict_select  the cut-off weight by radix selection (weights as ordered 32-bit keys,
 //                 digits of 11, 11 and 10 bits from the top), then the kept positions in
-//                 ascending order.  One cluster per (sequence, kv-head), every CTA a slice
-//                 of the positions, histograms and counts joined through distributed shared
-//                 memory; nothing is sorted and the order of the atomics cannot show.
+//                 ascending order.  One cluster per (sequence, kv-head) holds all its keys in
+//                 shared memory, histograms and counts joined through distributed shared memory;
+//                 the weights are read once, nothing is sorted, and the order of the atomics
+//                 cannot show (they count).
 //   evict_move    copies the rows: the bytes are what the operator cannot do without
 //                 (budget rows read and written, K and V), so each thread keeps eight
 //                 16-byte loads in flight; heads are the inner index, as they are in
 //                 memory, so that rows kept by several heads are read side by side.
-// The weights are read four times, three of them from L2 (4 bytes a token and head,
-// against 4 * d * element bytes moved per kept one).
 #include <string.h>
 
 #include <cooperative_groups.h>
@@ -28,7 +27,9 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kPer = 8;                       // consecutive positions of a thread when lists are written
+constexpr int kMaxCluster = 8;
+constexpr int kMaxKeys = 64;                  // keys a thread holds at most
+static_assert(kThreads * kMaxCluster * kMaxKeys >= STEM_MAX_KV_LEN, "a cluster holds the longest sequence");
 constexpr int kMoveThreads = 256;
 constexpr int kMovePieces = 8;                // 16-byte pieces a thread has in flight
 constexpr int kMoveRows = 512;                // (token, head) rows of a move CTA at most
@@ -36,6 +37,7 @@ static_assert(kBins == 4 * kThreads, "four bins per thread");
 
 struct EvictParams {
   EvictArgs a;
+  int kpt;             // keys of a select thread
   int move_tokens;     // tokens of a move CTA
 };
 
@@ -56,40 +58,30 @@ __device__ __forceinline__ int warp_inclusive(int x) {
   return x;
 }
 
-// Inclusive sum over the block and its total; `sums` is used again only after the next call's
-// first barrier.
-__device__ __forceinline__ int block_inclusive(int x, int* sums, int* total) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  x = warp_inclusive(x);
-  __syncthreads();
-  if (lane == 31) sums[warp] = x;
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int s = sums[w];
-    if (w < warp) before += s;
-    all += s;
-  }
-  *total = all;
-  return x + before;
-}
-
 struct SelectSmem {
   int hist[3][kBins];
   int sums[kWarps];
-  int digit, above;    // of the pass: the cut-off's digit, candidates in higher bins
-  int counts[2];       // of this CTA's slice: kept above the cut-off (forced ones too), equal to it
+  int digit, above;         // of the pass: the cut-off's digit, candidates in higher bins
+  int more[kWarps], same[kWarps];  // kept above the cut-off (forced ones too) and equal to it, by warp
+  int counts[2];            // of the CTA
 };
 
+// A CTA's slice is 512 * kpt positions, their keys in shared memory: warp w takes positions
+// [w, w + 1) * 32 * kpt of it, key e of lane l being number 32 e + l, so that loads are
+// coalesced, no key is another lane's, and ascending order is (warp, e, lane).
 __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__ EvictParams p) {
   const EvictArgs& a = p.a;
   __shared__ SelectSmem sm;
+  extern __shared__ uint32_t keys[];
+  const int kpt = p.kpt;  // a multiple of 8
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int unit = blockIdx.x / C, b = unit / a.Hkv, h = unit % a.Hkv;
-  const int tid = threadIdx.x;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const unsigned all = 0xffffffffu;
+  pdl_trigger();
+  for (int i = tid; i < 3 * kBins; i += kThreads) sm.hist[0][i] = 0;
+  pdl_wait();
 
   const int raw = __ldg(a.kv_lens + b);
   const int n = min(max(raw, 0), a.max_kv_len), m = min(n, a.budget);
@@ -110,15 +102,16 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
   }
 
   const int lo = a.sink, hi = n - a.recent, need = a.budget - a.sink - a.recent;  // candidates: [lo, hi)
-  const int slice = (n + C - 1) / C;
-  const int s0 = min(n, rank * slice), s1 = min(n, s0 + slice);
-  const int c0 = max(s0, lo), c1 = min(s1, hi);
-  for (int i = tid; i < 3 * kBins; i += kThreads) sm.hist[0][i] = 0;
+  const int first = rank * (kThreads * kpt) + warp * (32 * kpt) + lane;           // position of key 0
+  uint32_t* key = keys + warp * (32 * kpt) + lane;                                // key e at [32 * e]
+#pragma unroll 8
+  for (int e = 0; e < kpt; ++e) key[32 * e] = first + 32 * e < n ? order_key(w[first + 32 * e]) : 0u;
+  auto candidate = [&](int e) { return first + 32 * e >= lo && first + 32 * e < hi; };
   __syncthreads();
 
   // the cut-off key, digit by digit
   uint32_t cut = 0xFFFFFFFFu;  // no key is this large
-  int ties = 0, mine_above = 0, mine_equal = 0;
+  int ties = 0;
   if (need > 0) {
     uint32_t prefix = 0;
     int left = need;
@@ -126,112 +119,109 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
       int* hist = sm.hist[pass];
-#pragma unroll 4
-      for (int i0 = c0; i0 < c1; i0 += kThreads) {
-        const int i = i0 + tid;
-        const bool in = i < c1;
-        const uint32_t key = in ? order_key(w[i]) : 0u;
-        const int d = (key >> shift) & ((1 << bits) - 1);
-        if (pass == 0) {
-          // sign, exponent and two more bits: few bins hold nearly all keys, so the lanes of
-          // a warp that share one add once
-          const unsigned peers = __match_any_sync(0xffffffffu, in ? d : -1);
-          if (in && static_cast<int>(tid % 32) == __ffs(peers) - 1) atomicAdd(hist + d, __popc(peers));
-        } else if (in && (key >> (shift + bits)) == prefix) {
-          atomicAdd(hist + d, 1);
-        }
+#pragma unroll 8
+      for (int e = 0; e < kpt; ++e) {
+        const uint32_t k = key[32 * e];
+        const bool in = candidate(e) && (pass == 0 || (k >> (shift + bits)) == prefix);
+        const int d = in ? static_cast<int>((k >> shift) & ((1u << bits) - 1)) : -1;
+        // lanes that agree with the first one add once: equal weights are common (keys that
+        // nothing has looked at), and same-address atomics of a warp are done one by one
+        const unsigned on = __ballot_sync(all, in);
+        if (on == 0) continue;
+        const int lead = __ffs(on) - 1;
+        const unsigned peers = __ballot_sync(all, d == __shfl_sync(all, d, lead));
+        if (lane == lead) atomicAdd(hist + d, __popc(peers));
+        else if (in && !(peers >> lane & 1u)) atomicAdd(hist + d, 1);
       }
       cluster.sync();
       // bins from the top down: four per thread
-      const int top = kBins - 1 - 4 * tid;
-      int cnt[4], local[4], sum = 0;
+      const int bin = kBins - 4 - 4 * tid;
+      int4 c = make_int4(0, 0, 0, 0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        cnt[e] = 0;
-        local[e] = hist[top - e];
-        for (int r = 0; r < C; ++r) cnt[e] += cluster.map_shared_rank(hist, r)[top - e];
-        sum += cnt[e];
-      }
-      int total;
-      const int upto = block_inclusive(sum, sm.sums, &total);
-      int before = upto - sum;
-      if (before < left && left <= upto) {
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < C) {
+          const int4 x = *reinterpret_cast<const int4*>(cluster.map_shared_rank(hist, r) + bin);
+          c.x += x.x;
+          c.y += x.y;
+          c.z += x.z;
+          c.w += x.w;
+        }
+      const int cnt[4] = {c.w, c.z, c.y, c.x};
+      const int sum = c.x + c.y + c.z + c.w;
+      const int inc = warp_inclusive(sum);
+      if (lane == 31) sm.sums[warp] = inc;
+      __syncthreads();
+      int before = inc - sum;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) before += x < warp ? sm.sums[x] : 0;
+      if (before < left && left <= before + sum) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (before < left && left <= before + cnt[e]) {
-            sm.digit = top - e;
+            sm.digit = bin + 3 - e;
             sm.above = before;
           }
           before += cnt[e];
         }
       }
       __syncthreads();
-      const int digit = sm.digit;
+      prefix = (prefix << bits) | static_cast<uint32_t>(sm.digit);
       left -= sm.above;
-      int above = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) above += top - e > digit ? local[e] : 0;
-      block_inclusive(above, sm.sums, &total);
-      mine_above += total;
-      if (pass == 2) mine_equal = hist[digit];
-      prefix = (prefix << bits) | static_cast<uint32_t>(digit);
     }
     cut = prefix;
     ties = left;
   }
-  // kept tokens before this slice
-  const int forced = max(0, min(s1, lo) - s0) + max(0, s1 - max(s0, hi));
+  // which keys stay, the equal ones still open; counts by warp, CTA and rank
+  auto above = [&](int e) { return first + 32 * e < n && (!candidate(e) || key[32 * e] > cut); };
+  auto equal = [&](int e) { return candidate(e) && key[32 * e] == cut; };
+  int more = 0, same = 0;
+#pragma unroll 8
+  for (int e = 0; e < kpt; ++e) {
+    more += __popc(__ballot_sync(all, above(e)));
+    same += __popc(__ballot_sync(all, equal(e)));
+  }
+  if (lane == 0) {
+    sm.more[warp] = more;
+    sm.same[warp] = same;
+  }
+  __syncthreads();
+  int pos = 0, eq = 0, all_more = 0, all_same = 0;
+#pragma unroll
+  for (int x = 0; x < kWarps; ++x) {
+    pos += x < warp ? sm.more[x] : 0;
+    eq += x < warp ? sm.same[x] : 0;
+    all_more += sm.more[x];
+    all_same += sm.same[x];
+  }
   if (tid == 0) {
-    sm.counts[0] = mine_above + forced;
-    sm.counts[1] = mine_equal;
+    sm.counts[0] = all_more;
+    sm.counts[1] = all_same;
   }
   cluster.sync();
-  int eq = 0, pos = 0;
-  for (int r = 0; r < rank; ++r) {
-    const int* c = cluster.map_shared_rank(sm.counts, r);
-    pos += c[0];
-    eq += c[1];
-  }
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    if (r < rank) {
+      const int* c = cluster.map_shared_rank(sm.counts, r);
+      pos += c[0];
+      eq += c[1];
+    }
+  cluster.sync();  // the last look into another CTA's shared memory: each may leave from here on
+  // the list, in ascending order; of the equal ones the first `ties`
+  const unsigned below = (1u << lane) - 1u;
   pos += min(eq, ties);
-  // the list, in ascending order: equal weights by their index
-  for (int i0 = s0; i0 < s1; i0 += kThreads * kPer) {
-    const int base = i0 + tid * kPer;
-    float v[kPer];
-    uint32_t same = 0, more = 0;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int i = base + e;
-      v[e] = i < s1 ? w[i] : 0.f;
+#pragma unroll 8
+  for (int e = 0; e < kpt; ++e) {
+    const unsigned se = __ballot_sync(all, equal(e));
+    const bool take = above(e) || (equal(e) && eq + __popc(se & below) < ties);
+    const unsigned te = __ballot_sync(all, take);
+    if (take) {
+      const int at = pos + __popc(te & below);
+      keep[at] = first + 32 * e;
+      if (a.weights_out) wout[at] = w[first + 32 * e];
     }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int i = base + e;
-      if (i >= s1) continue;
-      const uint32_t key = order_key(v[e]);
-      if (i < lo || i >= hi || key > cut) more |= 1u << e;
-      else if (key == cut) same |= 1u << e;
-    }
-    int total;
-    int r = eq + block_inclusive(__popc(same), sm.sums, &total) - __popc(same);
-    eq += total;
-    uint32_t take = more;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e)
-      if (same >> e & 1u) {
-        if (r < ties) take |= 1u << e;
-        ++r;
-      }
-    int at = pos + block_inclusive(__popc(take), sm.sums, &total) - __popc(take);
-    pos += total;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e)
-      if (take >> e & 1u) {
-        keep[at] = base + e;
-        if (a.weights_out) wout[at] = v[e];
-        ++at;
-      }
+    pos += __popc(te);
+    eq += __popc(se);
   }
-  cluster.sync();  // no CTA leaves while another may read its shared memory
 }
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move(const __grid_constant__ EvictParams p) {
@@ -239,7 +229,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move(const __grid_constant
   __shared__ long long src_row[kMoveRows], dst_row[kMoveRows];  // in rows of the caches; -1: nothing to move
   const int blocks = (a.budget + p.move_tokens - 1) / p.move_tokens;
   const int b = blockIdx.x / blocks, i0 = (blockIdx.x % blocks) * p.move_tokens;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_trigger();
+  pdl_wait();
   const int m = min(min(max(__ldg(a.kv_lens + b), 0), a.max_kv_len), a.budget);
   const int tokens = min(p.move_tokens, m - i0);
   if (tokens <= 0) return;
@@ -291,33 +282,25 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move(const __grid_constant
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
   EvictParams p;
   p.a = a;
-  // CTAs per (sequence, kv-head): enough that the batch's clusters cover the SMs, as long as a
-  // CTA keeps 2048 positions
-  const long long units = static_cast<long long>(a.B) * a.Hkv;
+  // A cluster's shared memory holds a sequence: 8 keys a thread and as many CTAs as that needs
+  // (short chains of atomics, and long sequences of a ragged batch spread out), then more
+  // keys a thread.
+  const unsigned units = static_cast<unsigned>(a.B) * a.Hkv;
+  const int chunks = (a.max_kv_len + kThreads * 8 - 1) / (kThreads * 8);
   int C = 1;
-  while (C < 8 && units * C < 148 && a.max_kv_len / (2 * C) >= 2048) C *= 2;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * C));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = C;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select, p);
+  while (C < kMaxCluster && C < chunks) C *= 2;
+  p.kpt = 8 * ((chunks + C - 1) / C);
+  cudaError_t e = set_smem_once<evict_select>(kMaxKeys * kThreads * 4);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(evict_select, units * C, kThreads, static_cast<size_t>(p.kpt) * kThreads * 4, C, st, p);
   if (e != cudaSuccess) return e;
   // a move CTA's tokens: 8 pieces a thread, within its table of rows
   const int per_token = 2 * a.Hkv << a.row_shift;
   int tokens = kMoveThreads * kMovePieces / per_token;
   if (tokens * a.Hkv > kMoveRows) tokens = kMoveRows / a.Hkv;
   p.move_tokens = tokens < 1 ? 1 : tokens;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * ((a.budget + p.move_tokens - 1) / p.move_tokens));
-  cfg.blockDim = dim3(kMoveThreads);
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, evict_move, p);
+  const unsigned blocks = static_cast<unsigned>(a.B) * ((a.budget + p.move_tokens - 1) / p.move_tokens);
+  return launch_dependent(evict_move, blocks, kMoveThreads, 0, 1, st, p);
 }
 
 }  // namespace stem

@@ -349,6 +349,12 @@ __device__ __forceinline__ uint32_t e4m3x4_pairsum_h(uint32_t v) {
 // The same pair sums as floats.
 __device__ __forceinline__ float2 e4m3x4_pairsum(uint32_t v) { return h2_to_float2(e4m3x4_pairsum_h(v)); }
 
+// Programmatic dependent launch: a kernel launched with launch_dependent may start while
+// its predecessor in the stream still runs; it touches no memory before pdl_wait, which
+// returns when the predecessor has completed.  pdl_trigger lets the successor start.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Locate the sequence owning a global block row.
 __device__ __forceinline__ int seq_of_row(const Batch& bt, int row) {
   int b = 0;
@@ -371,6 +377,26 @@ __device__ __forceinline__ int tpd_k(double r, int N, double mu, int i) {
   double kk = f < static_cast<double>(m) ? static_cast<double>(m) : f;
   if (kk > static_cast<double>(i + 1)) kk = static_cast<double>(i + 1);
   return static_cast<int>(kk);
+}
+
+// Launch with programmatic stream serialisation, in clusters of `cluster` CTAs.
+template <typename K, typename... A>
+cudaError_t launch_dependent(K kern, unsigned grid, int threads, size_t smem, int cluster, cudaStream_t st,
+                             const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 #endif  // __CUDACC__
@@ -437,11 +463,14 @@ cudaError_t launch_bsa(const Batch& bt, const BsaArgs& a, bool fp8, bool paged, 
 bool make_map(CUtensorMap* m, const void* ptr, bool fp8, int d, int H, long long rows, int box_d, int box_rows);
 
 // Split of one decoding step over the CTAs.  The step's work is a line of 64-token tiles:
-// the prefix's units (kv-head, 16-row tile of all sequences' rows), then sequence after
-// sequence its own (kv-head, 16-row tile) units; every unit is as many tiles as its keys
-// have pages, and CTA c takes tiles [c * per, (c + 1) * per).
+// the prefix's units (head group, 16-row tile of all sequences' rows), then sequence after
+// sequence its own (head group, 16-row tile) units; every unit is as many tiles as its keys
+// have pages, and the CTAs take equal shares of the line (see stem_decode.cu).
 constexpr int kDecodeCtas = 296;      // two on each of 148 SMs
 constexpr int kDecodeRows = 16;       // query rows of a unit
+// What a unit costs beside its tiles (loading Q, joining the warps), in tiles: it counts as
+// that many empty ones on the line, so that a CTA with many short sequences gets fewer.
+constexpr int kDecodeUnitCost = 2;
 
 struct DecodeArgs {
   const void* q;
@@ -462,7 +491,6 @@ struct DecodeArgs {
   float* lse;
   // workspace
   uint32_t* status;
-  int32_t* cum;              // [B + 1] first tile of each sequence
   float* part_o;             // [slots, part_rows, d] unnormalised outputs of a CTA's share of a unit
   float2* part_ml;           // [slots, 16] running maximum (log2 domain) and sum
   float* scores;             // [B, Hkv, n * G, score_stride] log2-domain scores, or nullptr
@@ -471,7 +499,7 @@ struct DecodeArgs {
 };
 
 struct DecodeWs {
-  size_t status, cum, part_ml, part_o, scores, total;
+  size_t status, part_ml, part_o, scores, total;
   int part_rows;
   long long score_stride;
 };

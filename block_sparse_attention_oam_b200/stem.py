@@ -410,29 +410,33 @@ def _dtype_code(name: str) -> int:
 
 
 def _tensor(name: str, t, shape, dtype, device):
-    """A dense tensor of this shape (None: any length), type and device."""
-    if t.dtype != dtype or t.device != device or t.dim() != len(shape) or not t.is_contiguous() or any(
-            w is not None and w != g for w, g in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}; got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    """Address of a dense tensor of this shape (None: any length), type and device."""
+    if t.dtype == dtype and t.device == device and t.is_contiguous():
+        got = t.shape
+        if got == shape or (len(got) == len(shape) and all(w is None or w == g for w, g in zip(shape, got))):
+            return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}; got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}, contiguous: {t.is_contiguous()}")
 
 
 def _pages(name: str, c: PagedKV, num_seqs: int, Hkv: int, d: int, dtype, device):
-    shape = (None, PAGE_SIZE, Hkv, d)
-    k = _tensor(f"{name}.k_cache", c.k_cache, shape, dtype, device)
-    v = _tensor(f"{name}.v_cache", c.v_cache, tuple(c.k_cache.shape), dtype, device)
-    t = _tensor(f"{name}.block_table", c.block_table, (num_seqs, None), torch.int32, device)
-    return ctypes.byref(_Paged(k, v, t, PAGE_SIZE, c.block_table.shape[1], c.k_cache.shape[0]))
+    k, v, table = c.k_cache, c.v_cache, c.block_table
+    slots, width = k.shape[0], table.shape[-1]
+    shape = (slots, PAGE_SIZE, Hkv, d)
+    return _Paged(_tensor(f"{name}.k_cache", k, shape, dtype, device), _tensor(f"{name}.v_cache", v, shape, dtype, device),
+                  _tensor(f"{name}.block_table", table, (num_seqs, width), torch.int32, device), PAGE_SIZE, width, slots)
 
 
 def _call_on(device, stream, fn, *args) -> None:
     """Call the library on the tensors' device, on `stream` or that device's current one."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _call_on(device, stream, fn, *args)
     s = torch.cuda.current_stream(device) if stream is None else stream
-    _check(fn(*args, s.cuda_stream))
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, s.cuda_stream)
+    if status != STEM_OK:
+        _check(status)
 
 
 def decode_workspace(dec: Decode, device="cuda") -> torch.Tensor:
