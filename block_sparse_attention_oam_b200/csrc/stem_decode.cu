@@ -684,7 +684,7 @@ __device__ __forceinline__ void load_share(float (&x)[E], const float* src) {
 // it, from the lengths (decode_kernel triggers this launch after its own wait, when all that
 // came before it in the stream is complete), and all loads after it are independent.
 template <int D, bool SCORES, int WPR>
-__global__ void __launch_bounds__(kFinishThreads) decode_finish(const __grid_constant__ DecodeParams p, int row_blocks) {
+__global__ void __launch_bounds__(kFinishThreads, 3) decode_finish(const __grid_constant__ DecodeParams p, int row_blocks) {
   const DecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, G = a.G, R = a.n * G;
   constexpr int E = D / 32, RPB = kFinishThreads / 32 / WPR;  // columns of a lane, rows of a block

@@ -24,16 +24,21 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxKeys = 64;                  // keys a thread holds at most
+constexpr int kMinKeys = 16;                  // keys a thread holds, and at most
+constexpr int kMaxKeys = 128;
+constexpr int kBatch = 16;                    // of which read at a time
+static_assert(kMinKeys % kBatch == 0, "whole batches");
 static_assert(kThreads * kMaxCluster * kMaxKeys >= STEM_MAX_KV_LEN, "a cluster holds the longest sequence");
 constexpr int kMoveThreads = 256;
 constexpr int kMovePieces = 8;                // 16-byte pieces a thread has in flight
 constexpr int kMoveRows = 512;                // (token, head) rows of a move CTA at most
-static_assert(kBins == 4 * kThreads, "four bins per thread");
+constexpr int kCoarse = 64;                   // groups of bins that are looked at first
+constexpr int kFine = kBins / kCoarse;
+static_assert(kBins == 8 * kThreads && kThreads == 4 * kCoarse && kFine == 32 && kWarps >= kMaxCluster, "see evict_select");
 
 struct EvictParams {
   EvictArgs a;
@@ -41,7 +46,10 @@ struct EvictParams {
   int move_tokens;     // tokens of a move CTA
 };
 
-// Weights in an order that unsigned comparison follows; NaN as -inf, -0 as +0.
+// Weights in an order that unsigned comparison follows; NaN as -inf, -0 as +0.  They run
+// from that of -inf, 0x007FFFFF, to that of inf, 0xFF800000, so that two are free:
+constexpr uint32_t kNone = 0u;              // behind the last token
+constexpr uint32_t kForced = 0xFFFFFFFFu;   // kept whatever its weight
 __device__ __forceinline__ uint32_t order_key(float w) {
   if (!(w == w)) w = -INFINITY;
   const uint32_t u = w == 0.f ? 0u : __float_as_uint(w);
@@ -59,28 +67,39 @@ __device__ __forceinline__ int warp_inclusive(int x) {
 }
 
 struct SelectSmem {
-  int hist[3][kBins];
-  int sums[kWarps];
-  int digit, above;         // of the pass: the cut-off's digit, candidates in higher bins
-  int more[kWarps], same[kWarps];  // kept above the cut-off (forced ones too) and equal to it, by warp
-  int counts[2];            // of the CTA
+  int hist[2][kBins];              // passes 0 and 2, pass 1
+  int coarse[3][kCoarse];          // sums of 32 bins
+  int total[kCoarse];              // the same over the cluster, from the top down
+  int fine[kMaxCluster][kFine];    // the bins of one group, by CTA, from the top down
+  int more[kWarps], same[kWarps];  // keys above the cut-off (forced ones too) and equal to it, by warp
+  int counts[2];                   // of the CTA
 };
 
-// A CTA's slice is 512 * kpt positions, their keys in shared memory: warp w takes positions
-// [w, w + 1) * 32 * kpt of it, key e of lane l being number 32 e + l, so that loads are
-// coalesced, no key is another lane's, and ascending order is (warp, e, lane).
+// The entry that holds number `left` when the 32 lanes' counts are passed in lane order; takes
+// the counts before it from `left`.
+__device__ __forceinline__ int find_lane(int count, int* left) {
+  const int inc = warp_inclusive(count);
+  const unsigned hit = __ballot_sync(0xffffffffu, inc - count < *left && *left <= inc);
+  const int at = __ffs(hit) - 1;
+  *left -= __shfl_sync(0xffffffffu, inc - count, at);
+  return at;
+}
+
+// A CTA's slice is 256 * kpt positions (kpt by the sequence's length, so that the cluster's CTAs
+// share it evenly), their keys in shared memory: warp w takes positions [w, w + 1) * 32 * kpt
+// of it, key e of lane l being number 32 e + l, so that loads are coalesced, no key is another
+// lane's, and ascending order is (warp, e, lane).
 __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__ EvictParams p) {
   const EvictArgs& a = p.a;
   __shared__ SelectSmem sm;
   extern __shared__ uint32_t keys[];
-  const int kpt = p.kpt;  // a multiple of 8
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int unit = blockIdx.x / C, b = unit / a.Hkv, h = unit % a.Hkv;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const unsigned all = 0xffffffffu;
   pdl_trigger();
-  for (int i = tid; i < 3 * kBins; i += kThreads) sm.hist[0][i] = 0;
+  for (int i = tid; i < 2 * kBins; i += kThreads) sm.hist[0][i] = 0;
   pdl_wait();
 
   const int raw = __ldg(a.kv_lens + b);
@@ -102,15 +121,37 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
   }
 
   const int lo = a.sink, hi = n - a.recent, need = a.budget - a.sink - a.recent;  // candidates: [lo, hi)
+  const int kpt = kBatch * ((n + C * kThreads * kBatch - 1) / (C * kThreads * kBatch));  // p.kpt at most
   const int first = rank * (kThreads * kpt) + warp * (32 * kpt) + lane;           // position of key 0
   uint32_t* key = keys + warp * (32 * kpt) + lane;                                // key e at [32 * e]
-#pragma unroll 8
-  for (int e = 0; e < kpt; ++e) key[32 * e] = first + 32 * e < n ? order_key(w[first + 32 * e]) : 0u;
-  auto candidate = [&](int e) { return first + 32 * e >= lo && first + 32 * e < hi; };
+  for (int e0 = 0; e0 < kpt; e0 += kBatch) {
+    float v[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int i = first + 32 * (e0 + e);
+      v[e] = i >= lo && i < hi ? w[i] : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int i = first + 32 * (e0 + e);
+      key[32 * (e0 + e)] = i >= n ? kNone : (i < lo || i >= hi ? kForced : order_key(v[e]));
+    }
+  }
+  // Runs f(key) over the thread's keys, a batch read ahead: the compiler may not move a
+  // shared load over f's own stores and atomics.
+  auto each = [&](auto f) {
+    for (int e0 = 0; e0 < kpt; e0 += kBatch) {
+      uint32_t k[kBatch];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) k[e] = key[32 * (e0 + e)];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) f(k[e]);
+    }
+  };
   __syncthreads();
 
   // the cut-off key, digit by digit
-  uint32_t cut = 0xFFFFFFFFu;  // no key is this large
+  uint32_t cut = kForced - 1;  // no weight's key is this large
   int ties = 0;
   if (need > 0) {
     uint32_t prefix = 0;
@@ -118,68 +159,53 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-      int* hist = sm.hist[pass];
-#pragma unroll 8
-      for (int e = 0; e < kpt; ++e) {
-        const uint32_t k = key[32 * e];
-        const bool in = candidate(e) && (pass == 0 || (k >> (shift + bits)) == prefix);
-        const int d = in ? static_cast<int>((k >> shift) & ((1u << bits) - 1)) : -1;
-        // lanes that agree with the first one add once: equal weights are common (keys that
-        // nothing has looked at), and same-address atomics of a warp are done one by one
-        const unsigned on = __ballot_sync(all, in);
-        if (on == 0) continue;
-        const int lead = __ffs(on) - 1;
-        const unsigned peers = __ballot_sync(all, d == __shfl_sync(all, d, lead));
-        if (lane == lead) atomicAdd(hist + d, __popc(peers));
-        else if (in && !(peers >> lane & 1u)) atomicAdd(hist + d, 1);
-      }
+      int* hist = sm.hist[pass & 1];
+      each([&](uint32_t k) {
+        if (pass == 0 ? k != kNone && k != kForced : k >> (shift + bits) == prefix) atomicAdd(hist + ((k >> shift) & ((1u << bits) - 1)), 1);
+      });
+      __syncthreads();
+      // Reading all of the other CTAs' bins costs more than the rest (64 KB through distributed
+      // shared memory for each CTA: 10 us); so first the groups' sums, then the bins of one group.
+      const int4 x = *reinterpret_cast<const int4*>(hist + 8 * tid), y = *reinterpret_cast<const int4*>(hist + 8 * tid + 4);
+      int sum = ((x.x + x.y) + (x.z + x.w)) + ((y.x + y.y) + (y.z + y.w));
+      sum += __shfl_xor_sync(all, sum, 1);
+      sum += __shfl_xor_sync(all, sum, 2);
+      if (tid % 4 == 0) sm.coarse[pass][tid / 4] = sum;
       cluster.sync();
-      // bins from the top down: four per thread
-      const int bin = kBins - 4 - 4 * tid;
-      int4 c = make_int4(0, 0, 0, 0);
+      if (pass == 1)  // every CTA has done with pass 0's bins
+        for (int i = tid; i < kBins; i += kThreads) sm.hist[0][i] = 0;
+      int got = 0;
 #pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r)
-        if (r < C) {
-          const int4 x = *reinterpret_cast<const int4*>(cluster.map_shared_rank(hist, r) + bin);
-          c.x += x.x;
-          c.y += x.y;
-          c.z += x.z;
-          c.w += x.w;
-        }
-      const int cnt[4] = {c.w, c.z, c.y, c.x};
-      const int sum = c.x + c.y + c.z + c.w;
-      const int inc = warp_inclusive(sum);
-      if (lane == 31) sm.sums[warp] = inc;
+      for (int r = tid % 4; r < kMaxCluster; r += 4)
+        if (r < C) got += cluster.map_shared_rank(sm.coarse[pass], r)[kCoarse - 1 - tid / 4];
+      got += __shfl_xor_sync(all, got, 1);
+      got += __shfl_xor_sync(all, got, 2);
+      if (tid % 4 == 0) sm.total[tid / 4] = got;
       __syncthreads();
-      int before = inc - sum;
-#pragma unroll
-      for (int x = 0; x < kWarps; ++x) before += x < warp ? sm.sums[x] : 0;
-      if (before < left && left <= before + sum) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (before < left && left <= before + cnt[e]) {
-            sm.digit = bin + 3 - e;
-            sm.above = before;
-          }
-          before += cnt[e];
-        }
-      }
+      // every warp the same: lane l holds groups 2 l and 2 l + 1
+      const int c0 = sm.total[2 * lane], c1 = sm.total[2 * lane + 1];
+      const int pair = find_lane(c0 + c1, &left);
+      const int upper = __shfl_sync(all, c0, pair);
+      const int group = kCoarse - 1 - 2 * pair - (left > upper ? 1 : 0);
+      if (left > upper) left -= upper;
+      if (warp < C) sm.fine[warp][lane] = cluster.map_shared_rank(hist, warp)[kFine * group + kFine - 1 - lane];
       __syncthreads();
-      prefix = (prefix << bits) | static_cast<uint32_t>(sm.digit);
-      left -= sm.above;
+      int f = 0;
+      for (int r = 0; r < C; ++r) f += sm.fine[r][lane];
+      const int digit = kFine * group + kFine - 1 - find_lane(f, &left);
+      prefix = (prefix << bits) | static_cast<uint32_t>(digit);
     }
     cut = prefix;
     ties = left;
   }
   // which keys stay, the equal ones still open; counts by warp, CTA and rank
-  auto above = [&](int e) { return first + 32 * e < n && (!candidate(e) || key[32 * e] > cut); };
-  auto equal = [&](int e) { return candidate(e) && key[32 * e] == cut; };
   int more = 0, same = 0;
-#pragma unroll 8
-  for (int e = 0; e < kpt; ++e) {
-    more += __popc(__ballot_sync(all, above(e)));
-    same += __popc(__ballot_sync(all, equal(e)));
-  }
+  each([&](uint32_t k) {
+    more += k > cut ? 1 : 0;
+    same += k == cut ? 1 : 0;
+  });
+  more = __reduce_add_sync(all, more);
+  same = __reduce_add_sync(all, same);
   if (lane == 0) {
     sm.more[warp] = more;
     sm.same[warp] = same;
@@ -209,18 +235,31 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
   // the list, in ascending order; of the equal ones the first `ties`
   const unsigned below = (1u << lane) - 1u;
   pos += min(eq, ties);
-#pragma unroll 8
-  for (int e = 0; e < kpt; ++e) {
-    const unsigned se = __ballot_sync(all, equal(e));
-    const bool take = above(e) || (equal(e) && eq + __popc(se & below) < ties);
-    const unsigned te = __ballot_sync(all, take);
-    if (take) {
-      const int at = pos + __popc(te & below);
-      keep[at] = first + 32 * e;
-      if (a.weights_out) wout[at] = w[first + 32 * e];
+  for (int e0 = 0; e0 < kpt; e0 += kBatch) {
+    int at[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const uint32_t k = key[32 * (e0 + e)];
+      bool take = k > cut;
+      if (same > 0) {  // the same for the warp
+        const unsigned se = __ballot_sync(all, k == cut);
+        take = take || (k == cut && eq + __popc(se & below) < ties);
+        eq += __popc(se);
+      }
+      const unsigned te = __ballot_sync(all, take);
+      at[e] = take ? pos + __popc(te & below) : -1;
+      pos += __popc(te);
     }
-    pos += __popc(te);
-    eq += __popc(se);
+    float v[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e)
+      if (a.weights_out && at[e] >= 0) v[e] = w[first + 32 * (e0 + e)];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e)
+      if (at[e] >= 0) {
+        keep[at[e]] = first + 32 * (e0 + e);
+        if (a.weights_out) wout[at[e]] = v[e];
+      }
   }
 }
 
@@ -282,14 +321,13 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move(const __grid_constant
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
   EvictParams p;
   p.a = a;
-  // A cluster's shared memory holds a sequence: 8 keys a thread and as many CTAs as that needs
-  // (short chains of atomics, and long sequences of a ragged batch spread out), then more
-  // keys a thread.
+  // A cluster's shared memory holds a sequence: 16 keys a thread and as many CTAs as that
+  // needs (long sequences of a ragged batch are spread out), then more keys a thread.
   const unsigned units = static_cast<unsigned>(a.B) * a.Hkv;
-  const int chunks = (a.max_kv_len + kThreads * 8 - 1) / (kThreads * 8);
+  const int chunks = (a.max_kv_len + kThreads * kMinKeys - 1) / (kThreads * kMinKeys);
   int C = 1;
   while (C < kMaxCluster && C < chunks) C *= 2;
-  p.kpt = 8 * ((chunks + C - 1) / C);
+  p.kpt = kMinKeys * ((chunks + C - 1) / C);
   cudaError_t e = set_smem_once<evict_select>(kMaxKeys * kThreads * 4);
   if (e != cudaSuccess) return e;
   e = launch_dependent(evict_select, units * C, kThreads, static_cast<size_t>(p.kpt) * kThreads * 4, C, st, p);
