@@ -735,6 +735,23 @@ bool make_map(CUtensorMap* m, const void* ptr, bool fp8, int d, int H, long long
   return r == CUDA_SUCCESS;
 }
 
+bool make_map_rows(CUtensorMap* m, const void* ptr, bool fp8, int d, int G, int Hkv, long long tokens, int box_d,
+                   int box_tokens) {
+  EncodeTiledFn enc = get_encode();
+  if (enc == nullptr) return false;
+  const cuuint64_t es = fp8 ? 1 : 2, row = static_cast<cuuint64_t>(d) * es;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(Hkv),
+                        static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[3] = {row, row * G, row * G * Hkv};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(box_d), static_cast<cuuint32_t>(G), 1u,
+                       static_cast<cuuint32_t>(box_tokens)};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  CUresult r = enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                   const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 namespace {
 
 template <int D, int BN, bool FP8, bool PAGED, bool DENSE, int PART, bool SHKV, bool LSEX, bool SNAKE>

@@ -67,6 +67,7 @@ struct DecodeParams {
   int prefix_pages, prefix_span;  // pages of the prefix, its length on the line
   int gang;                  // CTAs that walk together, each with another kv-head of the same pages
   int gangs, head_groups;    // ctas / gang, Hkv / gang
+  PrefixPlan pre;            // gangs > 0: prefix_kernel has run before this one; prt is 0 then
 };
 
 __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int b) {
@@ -243,7 +244,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     tma_prefetch_map(&p.tk);
     tma_prefetch_map(&p.tv);
   }
-  pdl_wait();     // nothing of the caller's, nor the workspace, is touched before
+  // Nothing of the caller's, nor the workspace, is touched before the wait.  Behind
+  // prefix_kernel, which has made it, it comes last (see the end).
+  const bool behind = p.pre.gangs > 0;
+  if (!behind) pdl_wait();
   pdl_trigger();  // not earlier: decode_finish reads the lengths before its own wait
   int* cum = reinterpret_cast<int*>(merge);
   const int run = line_places<kThreads>(p, cum, warp_sums, [&](int raw) {
@@ -301,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     if (!alive)  // let the copies already issued land before the CTA can exit
       for (uint32_t q = it > C::NST ? it - C::NST : 0; q < it; ++q)
         for (int spin = 0; spin < 1000000 && !mbar_try_wait(full(q % C::NST), (q / C::NST) & 1); ++spin) {}
+    if (behind) pdl_wait();
     return;
   }
 
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       ml[warp * 16 + r0] = make_float2(m0, l0);
       ml[warp * 16 + r0 + 8] = make_float2(m1, l1);
     }
-    const bool direct = sg.own && sg.p0 == 0 && sg.p1 == sg.pages && p.prt == 0;
+    const bool direct = sg.own && sg.p0 == 0 && sg.p1 == sg.pages && a.prefix_len == 0;
     const long long slot = static_cast<long long>(gang_no + sg.unit) * p.gang + rank;
     // rounds of 4 rows x 128 columns (d 64: 8 rows x 64): few rows, few barriers
     constexpr int RPR = C::MROWS;
@@ -585,27 +590,50 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       consumer_sync();
     }
   }
+  // decode_finish waits for this kernel, which therefore does not end before prefix_kernel
+  if (behind) pdl_wait();
 }
 
-// The partials of one unit: slots `slot`, `slot + step`, ...
+// The partials of one row: its (m, l) at ml[i * ml_step], its output at o[i * o_step].
 struct Pieces {
-  long long slot;
-  int n, step;
+  const float2* ml;
+  const float* o;
+  long long ml_step, o_step;
+  int n;
 };
-__device__ __forceinline__ Pieces pieces_of(const DecodeParams& p, int start, int pages, int unit, int rank, int per) {
-  if (pages == 0) return Pieces{0, 0, 1};
-  const int c0 = (start + kDecodeUnitCost) / per, c1 = (start + kDecodeUnitCost + pages - 1) / per;
-  return Pieces{static_cast<long long>(c0 + unit) * p.gang + rank, c1 - c0 + 1, p.gang};
+// Pieces of a unit whose first tile lies at `first` on the line: CTA shares of `per`; its slots
+// start at (share + unit) * gang + rank, each of `rows` output rows.
+__device__ __forceinline__ Pieces pieces_of(const float2* ml, const float* o, int ml_rows, int rows, int d, int first,
+                                            int tiles, int unit, int gang, int rank, int per, int row) {
+  if (tiles == 0) return Pieces{nullptr, nullptr, 0, 0, 0};
+  const int c0 = first / per, c1 = (first + tiles - 1) / per;
+  const long long slot = static_cast<long long>(c0 + unit) * gang + rank;
+  return Pieces{ml + slot * ml_rows + row, o + (slot * rows + row) * d, static_cast<long long>(gang) * ml_rows,
+                static_cast<long long>(gang) * rows * d, c1 - c0 + 1};
 }
 __device__ __forceinline__ Pieces own_pieces(const DecodeParams& p, int per, int b, int base, int pages, int kvh,
-                                             int rtile) {
-  const int u = kvh / p.gang * p.rt + rtile;
-  return pieces_of(p, base + u * span_of(pages), pages, p.head_groups * (p.prt + b * p.rt) + u, kvh % p.gang, per);
+                                             int rr) {
+  const DecodeArgs& a = p.a;
+  const int u = kvh / p.gang * p.rt + rr / kDecodeRows;
+  return pieces_of(a.part_ml, a.part_o, kDecodeRows, a.part_rows, a.d, base + u * span_of(pages) + kDecodeUnitCost,
+                   pages, p.head_groups * (p.prt + b * p.rt) + u, p.gang, kvh % p.gang, per, rr % kDecodeRows);
 }
+// row: (token of the batch) * G + q-head of the group
 __device__ __forceinline__ Pieces prefix_pieces(const DecodeParams& p, int per, int kvh, int row) {
-  if (p.prt == 0) return Pieces{0, 0, 1};
+  const DecodeArgs& a = p.a;
+  const PrefixPlan& q = p.pre;
+  if (q.gangs > 0) {
+    const int tok = row / a.G, pair = tok / (2 * q.slot_tokens), in = tok % (2 * q.slot_tokens);
+    const int u = kvh / q.gang * q.pairs + pair;
+    return pieces_of(a.prefix_ml, a.prefix_o, 256, 256, a.d, u * (q.tiles + kPrefixUnitCost) + kPrefixUnitCost, q.tiles,
+                     u, q.gang, kvh % q.gang, q.per,
+                     in / q.slot_tokens * 128 + in % q.slot_tokens * a.G + row % a.G);
+  }
+  if (p.prt == 0) return Pieces{nullptr, nullptr, 0, 0, 0};
   const int u = kvh / p.gang * p.prt + row / kDecodeRows;
-  return pieces_of(p, u * (p.prefix_pages + kDecodeUnitCost), p.prefix_pages, u, kvh % p.gang, per);
+  return pieces_of(a.part_ml, a.part_o, kDecodeRows, a.part_rows, a.d,
+                   u * (p.prefix_pages + kDecodeUnitCost) + kDecodeUnitCost, p.prefix_pages, u, p.gang, kvh % p.gang,
+                   per, row % kDecodeRows);
 }
 // Pages of a sequence from its length on the line.
 __device__ __forceinline__ int pages_on_line(const DecodeParams& p, int length) {
@@ -623,22 +651,20 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// A row's partials, the own ones first: statistics of number i.
+// A row's partials, the own ones first.
 struct RowPieces {
   Pieces own, pre;
-  int own_row, pre_row;
   __device__ __forceinline__ int count() const { return own.n + pre.n; }
-  __device__ __forceinline__ long long slot(int i) const {
-    return i < own.n ? own.slot + static_cast<long long>(i) * own.step
-                     : pre.slot + static_cast<long long>(i - own.n) * pre.step;
+  __device__ __forceinline__ float2 stats(int i) const {
+    return i < own.n ? own.ml[i * own.ml_step] : pre.ml[(i - own.n) * pre.ml_step];
   }
-  __device__ __forceinline__ int row(int i) const { return i < own.n ? own_row : pre_row; }
+  __device__ __forceinline__ const float* out(int i) const {
+    return i < own.n ? own.o + i * own.o_step : pre.o + (i - own.n) * pre.o_step;
+  }
 };
 __device__ __forceinline__ RowPieces row_pieces(const DecodeParams& p, int per, int b, int base, int pages, int kvh,
                                                 int rr) {
-  const int pr = b * p.a.n * p.a.G + rr;
-  return RowPieces{own_pieces(p, per, b, base, pages, kvh, rr / kDecodeRows), prefix_pieces(p, per, kvh, pr),
-                   rr % kDecodeRows, pr % kDecodeRows};
+  return RowPieces{own_pieces(p, per, b, base, pages, kvh, rr), prefix_pieces(p, per, kvh, b * p.a.n * p.a.G + rr)};
 }
 
 // 2^(m - M), for a partial whose scores were all -inf 0 (and 1 where its sum is NaN: the
@@ -648,16 +674,16 @@ __device__ __forceinline__ float piece_factor(float2 v, float M) {
 }
 
 // Maximum and sum over a row's partials (all lanes get both).
-__device__ __forceinline__ float2 row_stats(const DecodeArgs& a, const RowPieces& q) {
+__device__ __forceinline__ float2 row_stats(const RowPieces& q) {
   const int lane = threadIdx.x % 32, n = q.count();
   float2 v = make_float2(-INFINITY, 0.f);
-  if (lane < n) v = a.part_ml[q.slot(lane) * kDecodeRows + q.row(lane)];
+  if (lane < n) v = q.stats(lane);
   float M = v.x;
-  for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, a.part_ml[q.slot(i) * kDecodeRows + q.row(i)].x);
+  for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, q.stats(i).x);
   M = warp_max(M);
   float L = piece_factor(v, M) * v.y;
   for (int i = lane + 32; i < n; i += 32) {
-    v = a.part_ml[q.slot(i) * kDecodeRows + q.row(i)];
+    v = q.stats(i);
     L += piece_factor(v, M) * v.y;
   }
   return make_float2(M, warp_sum(L));
@@ -706,19 +732,17 @@ __global__ void __launch_bounds__(kFinishThreads, 3) decode_finish(const __grid_
     const int base = cum[b], pages = pages_on_line(p, cum[b + 1] - base);
     const RowPieces q = row_pieces(p, per, b, base, pages, kvh, rr);
     const int n = q.count(), w = warp % WPR;
-    if (p.prt == 0 && n == 1) return;  // written by the CTA that saw all of it
+    if (a.prefix_len == 0 && n == 1) return;  // written by the CTA that saw all of it
     pdl_wait();
-    auto share_of = [&](int i) { return a.part_o + (q.slot(i) * a.part_rows + q.row(i)) * D + lane * E; };
-    auto stats_of = [&](int i) { return a.part_ml[q.slot(i) * kDecodeRows + q.row(i)]; };
     float x[PF][E];
     float2 v[PF];
 #pragma unroll
     for (int k = 0; k < PF; ++k)
       if (w + WPR * k < n) {
-        load_share(x[k], share_of(w + WPR * k));
-        v[k] = stats_of(w + WPR * k);
+        load_share(x[k], q.out(w + WPR * k) + lane * E);
+        v[k] = q.stats(w + WPR * k);
       }
-    const float2 st = row_stats(a, q);
+    const float2 st = row_stats(q);
     float o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
@@ -731,8 +755,8 @@ __global__ void __launch_bounds__(kFinishThreads, 3) decode_finish(const __grid_
       }
 #pragma unroll 4
     for (int i = w + WPR * PF; i < n; i += WPR) {
-      load_share(x[0], share_of(i));
-      const float f = piece_factor(stats_of(i), st.x);
+      load_share(x[0], q.out(i) + lane * E);
+      const float f = piece_factor(q.stats(i), st.x);
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] += f * x[0][e];
     }
@@ -805,7 +829,7 @@ __global__ void __launch_bounds__(kFinishThreads, 3) decode_finish(const __grid_
         for (int r = 0; r < 4; ++r)
           if (r < nr && j < len) x[r] = *reinterpret_cast<const float4*>(sc + r * a.score_stride);
         for (int r = warp; r < nr; r += kFinishThreads / 32) {
-          const float2 st = row_stats(a, row_pieces(p, per, b, base, pages, kvh, r0 + r));
+          const float2 st = row_stats(row_pieces(p, per, b, base, pages, kvh, r0 + r));
           // a row that sees nothing adds exp2(-inf - inf) = 0
           if (lane == 0) lse2[r] = st.y == 0.f ? INFINITY : st.x + log2f(st.y);
         }
@@ -866,14 +890,10 @@ cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st) {
   prm.a = a;
   const int R = a.n * a.G;
   prm.rt = (R + kDecodeRows - 1) / kDecodeRows;
-  prm.prt = a.prefix_len > 0 ? (a.B * R + kDecodeRows - 1) / kDecodeRows : 0;
+  prm.pre = plan_prefix(a.B, a.n, a.Hkv, a.G, a.prefix_len);
+  prm.prt = a.prefix_len > 0 && prm.pre.gangs == 0 ? (a.B * R + kDecodeRows - 1) / kDecodeRows : 0;
   prm.prefix_pages = (a.prefix_len + kTile - 1) / kTile;
-  // The gang: kv-heads are neighbours in memory (a page of one head is 64 pieces of 128 or
-  // 256 bytes), so CTAs that read the same pages at the same time, a head each, read whole
-  // DRAM rows.
-  prm.gang = 1;
-  for (int g = 2; g <= 8; ++g)
-    if (a.Hkv % g == 0) prm.gang = g;
+  prm.gang = gang_of(a.Hkv);
   prm.head_groups = a.Hkv / prm.gang;
   prm.prefix_span = prm.prt > 0 ? prm.head_groups * prm.prt * (prm.prefix_pages + kDecodeUnitCost) : 0;
   int dev = 0, sms = 0;
@@ -886,6 +906,7 @@ cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st) {
   prm.gangs = (2 * sms < kDecodeCtas ? 2 * sms : kDecodeCtas) / prm.gang;
   if (bound < prm.gangs) prm.gangs = static_cast<int>(bound);
   const bool scores = a.scores != nullptr;
+  if (prm.pre.gangs > 0 && (e = launch_prefix(a, prm.pre, fp8, st)) != cudaSuccess) return e;
   if (fp8) return scores ? run<128, true, true>(prm, st) : run<128, true, false>(prm, st);
   if (a.d == 128) return scores ? run<128, false, true>(prm, st) : run<128, false, false>(prm, st);
   return scores ? run<64, false, true>(prm, st) : run<64, false, false>(prm, st);

@@ -94,7 +94,9 @@ DecodeWs layout(const stem_decode_t* de) {
   const size_t B = de->num_seqs, Hkv = de->num_kv_heads, d = de->head_dim;
   const size_t R = static_cast<size_t>(de->q_len) * (de->num_q_heads / de->num_kv_heads);
   const size_t rt = (R + kDecodeRows - 1) / kDecodeRows;
-  const size_t prt = de->prefix_len > 0 ? (B * R + kDecodeRows - 1) / kDecodeRows : 0;
+  const PrefixPlan pre =
+      plan_prefix(de->num_seqs, de->q_len, de->num_kv_heads, de->num_q_heads / de->num_kv_heads, de->prefix_len);
+  const size_t prt = de->prefix_len > 0 && pre.gangs == 0 ? (B * R + kDecodeRows - 1) / kDecodeRows : 0;
   const size_t slots = kDecodeCtas + Hkv * (prt + B * rt);
   const size_t most = prt > 0 ? B * R : R;
   w.part_rows = static_cast<int>(most < kDecodeRows ? most : kDecodeRows);
@@ -103,6 +105,10 @@ DecodeWs layout(const stem_decode_t* de) {
   o = align256(o + slots * kDecodeRows * sizeof(float2));
   w.part_o = o;
   o = align256(o + slots * w.part_rows * d * 4);
+  w.prefix_ml = o;
+  o = align256(o + static_cast<size_t>(pre.slots) * 256 * sizeof(float2));
+  w.prefix_o = o;
+  o = align256(o + static_cast<size_t>(pre.slots) * 256 * d * 4);
   w.scores = o;
   w.score_stride = static_cast<long long>(de->max_kv_len + STEM_PAGE_SIZE - 1) / STEM_PAGE_SIZE * STEM_PAGE_SIZE;
   if (de->collect_weights) o = align256(o + B * Hkv * R * static_cast<size_t>(w.score_stride) * 4);
@@ -191,6 +197,8 @@ stem_status_t stem_decode(const stem_decode_t* dec, const void* q, const stem_pa
   a.status = at<uint32_t>(ws, w.status);
   a.part_ml = at<float2>(ws, w.part_ml);
   a.part_o = at<float>(ws, w.part_o);
+  a.prefix_ml = at<float2>(ws, w.prefix_ml);
+  a.prefix_o = at<float>(ws, w.prefix_o);
   a.scores = dec->collect_weights ? at<float>(ws, w.scores) : nullptr;
   a.score_stride = w.score_stride;
   a.part_rows = w.part_rows;

@@ -461,6 +461,10 @@ cudaError_t launch_bsa(const Batch& bt, const BsaArgs& a, bool fp8, bool paged, 
 // Tensor map over a token-major [rows, H, d] tensor: dims (d, H, rows), box (box_d, 1,
 // box_rows), 128-byte swizzle.  False when the driver refuses it.
 bool make_map(CUtensorMap* m, const void* ptr, bool fp8, int d, int H, long long rows, int box_d, int box_rows);
+// The same tensor seen as [tokens, Hkv, G, d]: dims (d, G, Hkv, tokens), box (box_d, G, 1,
+// box_tokens), so that a box holds the rows (token, q-head of one kv-head) one after another.
+bool make_map_rows(CUtensorMap* m, const void* ptr, bool fp8, int d, int G, int Hkv, long long tokens, int box_d,
+                   int box_tokens);
 
 // Split of one decoding step over the CTAs.  The step's work is a line of 64-token tiles:
 // the prefix's units (head group, 16-row tile of all sequences' rows), then sequence after
@@ -471,6 +475,31 @@ constexpr int kDecodeRows = 16;       // query rows of a unit
 // What a unit costs beside its tiles (loading Q, joining the warps), in tiles: it counts as
 // that many empty ones on the line, so that a CTA with many short sequences gets fewer.
 constexpr int kDecodeUnitCost = 2;
+
+// The kv-heads that CTAs walk side by side: neighbours in memory (a page of one head is 64
+// pieces of 128 or 256 bytes), so that they read whole DRAM rows between them.
+inline int gang_of(int Hkv) {
+  int gang = 1;
+  for (int g = 2; g <= 8; ++g)
+    if (Hkv % g == 0) gang = g;
+  return gang;
+}
+
+// The shared prefix's split when it runs on the tensor cores (stem_decode_prefix.cu): units
+// of (kv-head, pair of row tiles), each `tiles` 128-key tiles and kPrefixUnitCost empty ones
+// long on a gang member's line, of which every CTA takes `per`.
+constexpr int kPrefixCtas = 148;
+constexpr int kPrefixTile = 128;
+constexpr int kPrefixUnitCost = 2;
+constexpr int kPrefixMinRows = 32;
+struct PrefixPlan {
+  int gangs;                 // 0: the prefix is left to decode_kernel
+  int gang, head_groups;
+  int slot_tokens;           // tokens of a row tile
+  int pairs, tiles, per;
+  long long slots;           // partials of 256 rows each
+};
+PrefixPlan plan_prefix(int B, int n, int Hkv, int G, int prefix_len);
 
 struct DecodeArgs {
   const void* q;
@@ -496,15 +525,18 @@ struct DecodeArgs {
   float* scores;             // [B, Hkv, n * G, score_stride] log2-domain scores, or nullptr
   long long score_stride;
   int part_rows;
+  float* prefix_o;           // [plan.slots, 256, d], as part_o
+  float2* prefix_ml;         // [plan.slots, 256]
 };
 
 struct DecodeWs {
-  size_t status, part_ml, part_o, scores, total;
+  size_t status, part_ml, part_o, prefix_ml, prefix_o, scores, total;
   int part_rows;
   long long score_stride;
 };
 
 cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st);
+cudaError_t launch_prefix(const DecodeArgs& a, const PrefixPlan& plan, bool fp8, cudaStream_t st);
 
 struct EvictArgs {
   const int32_t* kv_lens;
