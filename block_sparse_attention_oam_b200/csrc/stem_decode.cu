@@ -54,10 +54,10 @@ struct Cfg {
   static constexpr int OFF_MERGE = NST * STAGE;
   static constexpr int OFF_ML = OFF_MERGE + MERGE;  // float2 [4][16]
   static constexpr int OFF_BAR = OFF_ML + 512;
-  static constexpr int SMEM = OFF_BAR + 512 + 1024;  // 1024: alignment
+  static constexpr int OFF_CUM = OFF_BAR + 512;     // the line: int [STEM_MAX_DECODE_SEQS + 1]
+  static constexpr int SMEM = OFF_CUM + (STEM_MAX_DECODE_SEQS + 1) * 4 + 1024;  // 1024: alignment
   static_assert(DCH >= 1 && NST >= 3 && NST <= 16, "ring");
   static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
-  static_assert(MERGE >= (STEM_MAX_DECODE_SEQS + 1) * 4, "the plan's table is built in the merge buffer");
 };
 
 struct DecodeParams {
@@ -68,7 +68,15 @@ struct DecodeParams {
   int gang;                  // CTAs that walk together, each with another kv-head of the same pages
   int gangs, head_groups;    // ctas / gang, Hkv / gang
   PrefixPlan pre;            // gangs > 0: prefix_kernel has run before this one; prt is 0 then
+  uint32_t g_magic;          // ceil(2^32 / G): x / G = umulhi(x, g_magic) for G > 1 (see div_g)
 };
+
+// x / G without a division: g_magic exceeds 2^32 / G by less than 1, so the product is off by
+// less than x / 2^32, which does not reach the next multiple of 1 / G for x < 2^32 / G (rows
+// number 2^24 at most, and G = 256 is exact).
+__device__ __forceinline__ int div_g(const DecodeParams& p, int x) {
+  return p.a.G == 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), p.g_magic));
+}
 
 __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int b) {
   return min(max(__ldg(a.kv_lens + b), 0), a.max_kv_len);
@@ -124,16 +132,28 @@ struct Seg {
   int p0, p1, pages, len;
 };
 
+// The sequence with cum[b] <= pos < cum[b + 1].
+__device__ __forceinline__ int find_seq(const DecodeParams& p, const int* cum, int pos) {
+  int lo = 0, hi = p.a.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (pos >= cum[mid + 1]) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
 // Walks the units of [t, end) in line order: the prefix's (head group, row tile), then
 // sequence after sequence (head group, row tile); a gang's member `rank` takes the head
-// group's head of that number.
+// group's head of that number.  b, base, span: the sequence it stands in, its first place and
+// its units' length (base = -1: none yet).
 struct Walk {
-  int t, end, b, base, len, rank;
-  __device__ __forceinline__ bool next(const DecodeParams& p, Seg* s) {
+  int t, end, b, rank, base, span, len;
+  __device__ __forceinline__ bool next(const DecodeParams& p, const int* cum, Seg* s) {
     while (t < end) {
       int at;  // place inside the unit, the empty tiles first
       if (t < p.prefix_span) {
-        const int span = p.prefix_pages + kDecodeUnitCost, u = t / span;
+        const int length = p.prefix_pages + kDecodeUnitCost, u = t / length;
         s->own = false;
         s->unit = u;
         s->kvh = u / p.prt * p.gang + rank;
@@ -141,20 +161,22 @@ struct Walk {
         s->b = 0;
         s->pages = p.prefix_pages;
         s->len = p.a.prefix_len;
-        at = t - u * span;
+        at = t - u * length;
       } else {
         const int units = p.head_groups * p.rt;
-        int span = span_of(pages_of(len));
-        while (t >= base + span * units) {
-          base += span * units;
-          len = clamp_len(p.a, ++b);
-          span = span_of(pages_of(len));
+        if (base < 0) b = find_seq(p, cum, t);
+        if (base < 0 || t >= cum[b + 1]) {
+          while (t >= cum[b + 1]) ++b;
+          base = cum[b];
+          span = (cum[b + 1] - base) / units;
+          len = clamp_len(p.a, b);
         }
         const int u = (t - base) / span;
         s->own = true;
+        const int hg = p.rt == 1 ? u : u / p.rt;
         s->unit = p.head_groups * (p.prt + b * p.rt) + u;
-        s->kvh = u / p.rt * p.gang + rank;
-        s->rtile = u % p.rt;
+        s->kvh = hg * p.gang + rank;
+        s->rtile = u - hg * p.rt;
         s->b = b;
         s->pages = span - kDecodeUnitCost;
         s->len = len;
@@ -170,6 +192,12 @@ struct Walk {
   }
 };
 
+// A 4-byte load that stays where it is written (before the barriers that follow).
+__device__ __forceinline__ uint32_t ld_early(const void* at) {
+  uint32_t r;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(r) : "l"(at));
+  return r;
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -226,7 +254,6 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 128 + 8 * s; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 256);
-  int* plan = reinterpret_cast<int*>(smem + C::OFF_BAR + 260);        // start sequence, its first tile, total
   int* warp_sums = reinterpret_cast<int*>(smem + C::OFF_BAR + 288);   // [5]
   const DecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -238,8 +265,6 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       mbar_init(empty(s), 4);
     }
     *abort_flag = 0;
-    plan[0] = 0;
-    plan[1] = p.prefix_span;
     mbar_fence_init();
     tma_prefetch_map(&p.tk);
     tma_prefetch_map(&p.tv);
@@ -249,58 +274,77 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
   const bool behind = p.pre.gangs > 0;
   if (!behind) pdl_wait();
   pdl_trigger();  // not earlier: decode_finish reads the lengths before its own wait
-  int* cum = reinterpret_cast<int*>(merge);
+  int* cum = reinterpret_cast<int*>(smem + C::OFF_CUM);
   const int run = line_places<kThreads>(p, cum, warp_sums, [&](int raw) {
     if (blockIdx.x == 0 && (raw < 0 || raw > a.max_kv_len)) atomicOr(a.status, kStatusBounds);
   });
   const int gang_no = static_cast<int>(blockIdx.x) / p.gang, rank = static_cast<int>(blockIdx.x) % p.gang;
   const int per = (run + p.gangs - 1) / p.gangs;
   const int t0 = min(run, gang_no * per), t1 = min(run, t0 + per);
-  for (int b = tid; b < a.B; b += kThreads) {
-    if (cum[b] <= t0 && t0 < cum[b + 1]) {
-      plan[0] = b;
-      plan[1] = cum[b];
-    }
-  }
-  __syncthreads();
-  Walk walk{t0, t1, plan[0], plan[1], clamp_len(a, plan[0]), rank};
-  Seg sg;
-
   if (warp == 4) {
     // ------------------------------------------------------------ producer
+    // 32 places of the line at a time, a lane each: which unit and page it is, and the page's
+    // slot, looked up one batch ahead so that short units wait for no lookup.
+    struct Place {
+      int kvh, slot;
+      bool tile;
+    };
+    auto look = [&](int pos) {
+      Place q{0, 0, false};
+      if (pos >= t1) return q;
+      const int32_t* table = a.prefix_table;
+      int at;
+      if (pos < p.prefix_span) {
+        const int length = p.prefix_pages + kDecodeUnitCost, u = pos / length;
+        q.kvh = u / p.prt * p.gang + rank;
+        at = pos - u * length;
+      } else {
+        const int lo = find_seq(p, cum, pos);
+        const int base = cum[lo], span = (cum[lo + 1] - base) / (p.head_groups * p.rt), u = (pos - base) / span;
+        q.kvh = (p.rt == 1 ? u : u / p.rt) * p.gang + rank;
+        at = pos - base - u * span;
+        table = a.table + static_cast<long long>(lo) * a.max_pages;
+      }
+      q.tile = at >= kDecodeUnitCost;
+      if (q.tile) q.slot = __ldg(table + at - kDecodeUnitCost);
+      return q;
+    };
     uint32_t it = 0;
     bool alive = true;
-    while (alive && walk.next(p, &sg)) {
-      const int32_t* table = sg.own ? a.table + static_cast<long long>(sg.b) * a.max_pages : a.prefix_table;
-      for (int q0 = sg.p0; q0 < sg.p1 && alive; q0 += 32) {
-        int slot = 0;
-        if (q0 + lane < sg.p1) {
-          slot = __ldg(table + q0 + lane);
-          if (slot < 0 || slot >= a.num_slots) {
-            atomicOr(a.status, kStatusBounds);
-            slot = 0;
+    Place ahead = look(t0 + lane);
+    for (int x = t0; x < t1 && alive; x += 32) {
+      const Place now = ahead;
+      bool looked = false;
+      int issued = 0;
+      int mine = now.slot;
+      if (mine < 0 || mine >= a.num_slots) {
+        atomicOr(a.status, kStatusBounds);
+        mine = 0;
+      }
+      for (unsigned todo = __ballot_sync(all, now.tile); todo; todo &= todo - 1, ++it) {
+        const int l = __ffs(todo) - 1;
+        const int row = __shfl_sync(all, mine, l) * kTile, kvh = __shfl_sync(all, now.kvh, l);
+        const int st = it % C::NST;
+        const bool ok = mbar_wait(empty(st), ((it / C::NST) & 1) ^ 1, abort_flag, a.status);
+        if (!__all_sync(all, ok)) {
+          alive = false;
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full(st), C::STAGE);
+          const uint32_t dst = sring + st * C::STAGE;
+#pragma unroll
+          for (int c = 0; c < C::DCH; ++c) {
+            tma_load_3d(dst + c * C::CHUNK, &p.tk, full(st), c * C::CH, kvh, row);
+            tma_load_3d(dst + C::TILE + c * C::CHUNK, &p.tv, full(st), c * C::CH, kvh, row);
           }
         }
-        const int cnt = min(32, sg.p1 - q0);
-        for (int q = 0; q < cnt; ++q, ++it) {
-          const int row = __shfl_sync(all, slot, q) * kTile;
-          const int st = it % C::NST;
-          const bool ok = mbar_wait(empty(st), ((it / C::NST) & 1) ^ 1, abort_flag, a.status);
-          if (!__all_sync(all, ok)) {
-            alive = false;
-            break;
-          }
-          if (lane == 0) {
-            mbar_arrive_expect_tx(full(st), C::STAGE);
-            const uint32_t dst = sring + st * C::STAGE;
-#pragma unroll
-            for (int c = 0; c < C::DCH; ++c) {
-              tma_load_3d(dst + c * C::CHUNK, &p.tk, full(st), c * C::CH, sg.kvh, row);
-              tma_load_3d(dst + C::TILE + c * C::CHUNK, &p.tv, full(st), c * C::CH, sg.kvh, row);
-            }
-          }
+        if (++issued == C::NST) {  // the ring is filled before the look ahead
+          ahead = look(x + 32 + lane);
+          looked = true;
         }
       }
+      if (!looked) ahead = look(x + 32 + lane);
     }
     if (!alive)  // let the copies already issued land before the CTA can exit
       for (uint32_t q = it > C::NST ? it - C::NST : 0; q < it; ++q)
@@ -317,8 +361,34 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
   const uint32_t v_row = static_cast<uint32_t>(warp * 16 + (mi & 1) * 8 + (lane & 7)) * 128;
   const int k_sub = FP8 ? mi >> 1 : mi & 1, v_sub = mi >> 1;
   const int sw = lane & 7;
+  // Q fragments of a unit's rows
+  uint32_t qf[D / 16][4];
+  auto load_q = [&](const Seg& g) {
+    const int first = g.rtile * kDecodeRows;
+    const int nrows = min(kDecodeRows, (g.own ? a.n * G : a.B * a.n * G) - first);
+    const unsigned char* qb = static_cast<const unsigned char*>(a.q);
+    const int g0 = (g.own ? g.b * a.n * G : 0) + first + r0, g1 = g0 + 8;
+    const int k0 = div_g(p, g0), k1 = div_g(p, g1);
+    const unsigned char* q0 = qb + (static_cast<long long>(k0) * a.Hq + g.kvh * G + g0 - k0 * G) * (D * C::ES) + qd * 4;
+    const unsigned char* q1 = qb + (static_cast<long long>(k1) * a.Hq + g.kvh * G + g1 - k1 * G) * (D * C::ES) + qd * 4;
+    const bool on0 = r0 < nrows, on1 = r0 + 8 < nrows;
+    constexpr int STEP = FP8 ? 16 : 32;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      qf[k][0] = on0 ? ld_early(q0 + k * STEP) : 0u;
+      qf[k][1] = on1 ? ld_early(q1 + k * STEP) : 0u;
+      if (!FP8) {
+        qf[k][2] = on0 ? ld_early(q0 + k * STEP + 16) : 0u;
+        qf[k][3] = on1 ? ld_early(q1 + k * STEP + 16) : 0u;
+      }
+    }
+  };
+  Walk walk{t0, t1, 0, rank, -1, 0, 0};
+  Seg sg;
+  bool have = walk.next(p, cum, &sg);
+  if (have) load_q(sg);
   uint32_t it = 0;
-  while (walk.next(p, &sg)) {
+  while (have) {
     const int rows_all = sg.own ? a.n * G : a.B * a.n * G;
     const int first = sg.rtile * kDecodeRows;
     const int nrows = min(kDecodeRows, rows_all - first);
@@ -326,34 +396,18 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     // keys that the unit's first and last row, and this thread's two rows, see
     auto limit_of = [&](int r) {
       if (!sg.own) return sg.len;
-      return max(0, sg.len - a.n + (first + r) / G + 1);
+      return max(0, sg.len - a.n + div_g(p, first + r) + 1);
     };
     const int lim_lo = limit_of(0), lim_hi = limit_of(nrows - 1);
     const int lim0 = limit_of(min(r0, nrows - 1)), lim1 = limit_of(min(r0 + 8, nrows - 1));
-    // Q fragments
-    uint32_t qf[D / 16][4];
-    {
-      const unsigned char* qb = static_cast<const unsigned char*>(a.q);
-      const int g0 = row_base + r0, g1 = row_base + r0 + 8;
-      const unsigned char* q0 =
-          qb + (static_cast<long long>(g0 / G) * a.Hq + sg.kvh * G + g0 % G) * D * C::ES + qd * 4;
-      const unsigned char* q1 =
-          qb + (static_cast<long long>(g1 / G) * a.Hq + sg.kvh * G + g1 % G) * D * C::ES + qd * 4;
+    if (FP8) {  // four codes a word: the k positions 2 qd, + 1 and 2 qd + 8, + 9 of the fragment
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        if (FP8) {
-          const uint32_t x = r0 < nrows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 16)) : 0u;
-          const uint32_t y = r0 + 8 < nrows ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 16)) : 0u;
-          qf[k][0] = e4m3x2_to_h2(x & 0xFFFFu);
-          qf[k][2] = e4m3x2_to_h2(x >> 16);
-          qf[k][1] = e4m3x2_to_h2(y & 0xFFFFu);
-          qf[k][3] = e4m3x2_to_h2(y >> 16);
-        } else {
-          qf[k][0] = r0 < nrows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 32)) : 0u;
-          qf[k][2] = r0 < nrows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 32 + 16)) : 0u;
-          qf[k][1] = r0 + 8 < nrows ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 32)) : 0u;
-          qf[k][3] = r0 + 8 < nrows ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 32 + 16)) : 0u;
-        }
+        const uint32_t x = qf[k][0], y = qf[k][1];
+        qf[k][0] = e4m3x2_to_h2(x & 0xFFFFu);
+        qf[k][2] = e4m3x2_to_h2(x >> 16);
+        qf[k][1] = e4m3x2_to_h2(y & 0xFFFFu);
+        qf[k][3] = e4m3x2_to_h2(y >> 16);
       }
     }
     float* srow = nullptr;
@@ -509,8 +563,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
           // The rows' limits differ inside these 16 tokens (drafted tokens): one product per
           // new token, taken by its rows alone, so that a row is never touched by a V row
           // that it does not see (0 * NaN).
-          const int ta = first / G, tb = (first + nrows - 1) / G;
-          const int mine0 = (first + min(r0, nrows - 1)) / G, mine1 = (first + min(r0 + 8, nrows - 1)) / G;
+          const int ta = div_g(p, first), tb = div_g(p, first + nrows - 1);
+          const int mine0 = div_g(p, first + min(r0, nrows - 1)), mine1 = div_g(p, first + min(r0 + 8, nrows - 1));
           for (int t = ta; t <= tb; ++t)
             pv(std::true_type{}, true, max(0, sg.len - a.n + t + 1), mine0 == t, mine1 == t);
         }
@@ -518,6 +572,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(st));
     }
+
+    // the next unit's Q on its way while this one is joined
+    const Seg was = sg;
+    have = walk.next(p, cum, &sg);
+    if (have) load_q(sg);
 
     // join the four warps' shares
     l0 += __shfl_xor_sync(all, l0, 1);
@@ -528,8 +587,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       ml[warp * 16 + r0] = make_float2(m0, l0);
       ml[warp * 16 + r0 + 8] = make_float2(m1, l1);
     }
-    const bool direct = sg.own && sg.p0 == 0 && sg.p1 == sg.pages && a.prefix_len == 0;
-    const long long slot = static_cast<long long>(gang_no + sg.unit) * p.gang + rank;
+    const bool direct = was.own && was.p0 == 0 && was.p1 == was.pages && a.prefix_len == 0;
+    const long long slot = static_cast<long long>(gang_no + was.unit) * p.gang + rank;
     // rounds of 4 rows x 128 columns (d 64: 8 rows x 64): few rows, few barriers
     constexpr int RPR = C::MROWS;
 #pragma unroll
@@ -574,10 +633,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         }
         if (direct) {
           const int g = row_base + r;
-          const long long tok = g / G;
-          const int h = sg.kvh * G + g % G;
+          const int tok = div_g(p, g);
+          const int h = was.kvh * G + g - tok * G;
           const float inv = M == -INFINITY && L == 0.f ? 0.f : a.v_scale / L;  // nothing seen: o = 0
-          *reinterpret_cast<uint2*>(static_cast<unsigned char*>(a.out) + ((tok * a.Hq + h) * D + col) * 2) =
+          *reinterpret_cast<uint2*>(static_cast<unsigned char*>(a.out) + ((static_cast<long long>(tok) * a.Hq + h) * D + col) * 2) =
               make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
           if (a.lse != nullptr && col == 0)
             a.lse[static_cast<long long>(h) * a.B * a.n + tok] =
@@ -710,7 +769,7 @@ __device__ __forceinline__ void load_share(float (&x)[E], const float* src) {
 // it, from the lengths (decode_kernel triggers this launch after its own wait, when all that
 // came before it in the stream is complete), and all loads after it are independent.
 template <int D, bool SCORES, int WPR>
-__global__ void __launch_bounds__(kFinishThreads, 3) decode_finish(const __grid_constant__ DecodeParams p, int row_blocks) {
+__global__ void __launch_bounds__(kFinishThreads, SCORES ? 3 : 4) decode_finish(const __grid_constant__ DecodeParams p, int row_blocks) {
   const DecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, G = a.G, R = a.n * G;
   constexpr int E = D / 32, RPB = kFinishThreads / 32 / WPR;  // columns of a lane, rows of a block
@@ -893,6 +952,7 @@ cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st) {
   prm.pre = plan_prefix(a.B, a.n, a.Hkv, a.G, a.prefix_len);
   prm.prt = a.prefix_len > 0 && prm.pre.gangs == 0 ? (a.B * R + kDecodeRows - 1) / kDecodeRows : 0;
   prm.prefix_pages = (a.prefix_len + kTile - 1) / kTile;
+  prm.g_magic = a.G > 1 ? static_cast<uint32_t>(((1ull << 32) + a.G - 1) / a.G) : 0u;
   prm.gang = gang_of(a.Hkv);
   prm.head_groups = a.Hkv / prm.gang;
   prm.prefix_span = prm.prt > 0 ? prm.head_groups * prm.prt * (prm.prefix_pages + kDecodeUnitCost) : 0;

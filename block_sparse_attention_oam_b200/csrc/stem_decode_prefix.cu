@@ -12,9 +12,12 @@
 //   warp 0      TMA producer: the unit's Q tiles, then K and V tiles through shared rings
 //   warp 1      MMA issuer: S = Q K^T into a slot's TMEM columns, O += P V with P in TMEM;
 //               the two slots take turns, one's softmax under the other's products
-//   warps 2..9  softmax, one thread per row, four warps per slot: running maximum raised
-//               lazily, sums of the unrounded P in float32
-//   warps 10,11 (FP8) widen V's codes to f16 in shared memory: with P in f16 the product
+//   warps 2..17 softmax, eight warps per slot, two threads per row with 64 of the tile's 128
+//               keys each: with one thread per row and two warps per scheduler the latency
+//               of the exponentials' chain, not their rate, set the pace (3.0 us for a tile of
+//               256 rows; 1.5 us of products).  The halves agree on the row's running maximum
+//               through shared memory; it is raised lazily; sums of the unrounded P in float32
+//   warps 18,19 (FP8) widen V's codes to f16 in shared memory: with P in f16 the product
 //               carries P to 2^-11, where an e4m3 P would lose 2^-4 of every weight; S stays
 //               an e4m3 product, which is exact
 // BF16 rounds P to bf16, as V is.  V rows behind the prefix's end (the rest of its last page)
@@ -48,12 +51,12 @@ struct Cfg {
   static constexpr int OFF_V = OFF_K + NK * TILE;
   static constexpr int OFF_H = OFF_V + NV * TILE;
   static constexpr int OFF_BAR = OFF_H + NH * VTILE;
-  static constexpr int SMEM = OFF_BAR + 512 + 1024;
+  static constexpr int OFF_MAX = OFF_BAR + 512;     // float [2][2 slots][2 halves][128 rows]
+  static constexpr int SMEM = OFF_MAX + 4096 + 1024;
   static_assert(SMEM <= 227 * 1024 && SMEM > 114 * 1024, "one CTA per SM");
-  static constexpr int THREADS = 32 * (FP8 ? 12 : 10);
+  static constexpr int THREADS = 32 * (FP8 ? 20 : 18);
   static constexpr int S_STEPS = D * ES / 32;
   static constexpr int PV_STEPS = kBN / 16;
-  static constexpr int P_COLS = kBN / 2;            // 16-bit P, packed
   static constexpr uint32_t IDESC_S = instr_desc(FP8 ? 0u : 1u, 0, 0, kRows, kBN);
   static constexpr uint32_t IDESC_PV = instr_desc(FP8 ? 0u : 1u, 0, 1, kRows, D);  // f16 or bf16
 };
@@ -109,6 +112,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// One whole 32-byte sector.
+__device__ __forceinline__ void st_global32(float* at, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
   uint4 v;
@@ -168,6 +177,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1) prefix_kernel(const _
   auto h_full = [&](int t) { return b0 + 208 + 8 * t; };
   auto h_empty = [&](int t) { return b0 + 224 + 8 * t; };
   const uint32_t bar_drain = b0 + 240;
+  auto agreed = [&](int s, int q) { return b0 + 288 + 8 * (4 * s + q); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 256);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 264);
 
@@ -178,7 +188,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1) prefix_kernel(const _
       mbar_init(q_full(s), 1);
       mbar_init(q_empty(s), 1);
       mbar_init(s_full(s), 1);
-      mbar_init(p_full(s), 4);
+      mbar_init(p_full(s), 8);
+      for (int q = 0; q < 4; ++q) mbar_init(agreed(s, q), 2);
       mbar_init(o_done(s), 1);
     }
     for (int t = 0; t < C::NK; ++t) {
@@ -366,15 +377,30 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1) prefix_kernel(const _
       for (int spin = 0; spin < 4000000 && !mbar_try_wait(bar_drain, 0); ++spin) {}
     }
     __syncwarp();
-  } else if (warp < 10) {
+  } else if (warp < 18) {
     // ------------------------------------------------------------ softmax
-    const int slot = (warp - 2) / 4, quad = warp % 4;
+    constexpr int HN = kBN / 2;                      // keys of a half
+    const int slot = (warp - 2) / 8, half = (warp - 2) / 4 % 2, quad = warp % 4;
     const int r = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t my_S = tmem + 256 * slot + lane_off, my_O = my_S + 128;
+    const uint32_t my_S = tmem + 256 * slot + lane_off;
+    const uint32_t my_O = my_S + 128 + half * (D / 2);
+    volatile float* my_max = reinterpret_cast<volatile float*>(smem + C::OFF_MAX) + (slot * 2 + half) * 128 + r;
+    volatile float* other_max = reinterpret_cast<volatile float*>(smem + C::OFF_MAX) + (slot * 2 + 1 - half) * 128 + r;
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-    uint32_t gb = 0, ot = 0, it = 0;
+    uint32_t gb = 0, ga = 0, ot = 0, it = 0;
     bool alive = true;
+    // Exchanges a value with the row's other thread.  Two buffers in turn: a thread writes one
+    // again only after the exchange in between, to which the other came after it had read.
+    auto swap = [&](float mine, float* theirs) -> bool {
+      const int at = ga & 1 ? 512 : 0;
+      my_max[at] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(agreed(slot, quad));
+      if (!warp_wait(agreed(slot, quad), ga++ & 1, abort_flag, p.status)) return false;
+      *theirs = other_max[at];
+      return true;
+    };
     while (alive && walk.next(p, &sg)) {
       const int n = sg.j1 - sg.j0;
       if (slot >= sg.ns) {
@@ -389,15 +415,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1) prefix_kernel(const _
           break;
         }
         tc_fence_after();
-        uint32_t sr[kBN];
+        uint32_t sr[HN];
 #pragma unroll
-        for (int c = 0; c < kBN / 32; ++c) tmem_ld32(my_S + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+        for (int c = 0; c < HN / 32; ++c)
+          tmem_ld32(my_S + half * HN + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
         tmem_wait_ld();
         const int valid = p.len - (sg.j0 + jj) * kBN;
         if (valid < kBN) {
 #pragma unroll
-          for (int c = 0; c < kBN; ++c)
-            if (c >= valid) sr[c] = __float_as_uint(-INFINITY);
+          for (int c = 0; c < HN; ++c)
+            if (half * HN + c >= valid) sr[c] = __float_as_uint(-INFINITY);
           if constexpr (!FP8) {
             // V's rows behind the end
             const uint32_t tv = it % C::NV;
@@ -405,7 +432,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1) prefix_kernel(const _
               alive = false;
               break;
             }
-            if (r >= valid)
+            if (half == 0 && r >= valid)
               for (int c = 0; c < C::DCH; ++c)
                 for (int x = 0; x < 8; ++x) st_shared16(sV + tv * C::TILE + c * C::CHUNK + r * 128 + x * 16, 0, 0, 0, 0);
             fence_async_shared();
@@ -413,11 +440,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1) prefix_kernel(const _
         }
         float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < kBN; c += 8)
+        for (int c = 0; c < HN; c += 8)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             mq[q] = max3f(mq[q], __uint_as_float(sr[c + 2 * q]), __uint_as_float(sr[c + 2 * q + 1]));
-        const float mx = fmaxf(max3f(mq[0], mq[1], mq[2]), mq[3]);
+        // After the exchange both halves of S are in registers, so P may be written over them
+        float mx = fmaxf(max3f(mq[0], mq[1], mq[2]), mq[3]), theirs;
+        tc_fence_before();
+        if (!swap(mx, &theirs)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        mx = fmaxf(mx, theirs);
         const float m_new = fmaxf(m_run, mx * p.scale_log2);
         const bool resc = m_new > m_run + 8.0f;
         const float m_use = resc ? m_new : m_run;
@@ -427,23 +462,22 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1) prefix_kernel(const _
         float2 sq[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) sq[q] = make_float2(0.f, 0.f);
-        // P packed in place over the first P_COLS registers
+        // P packed in place over the first half of the registers
 #pragma unroll
-        for (int u = 0; u < kBN / 2; ++u) {
+        for (int u = 0; u < HN / 2; ++u) {
           const float2 y = fma2(make_float2(__uint_as_float(sr[2 * u]), __uint_as_float(sr[2 * u + 1])), sc2, bias2);
           const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
           sr[u] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
           sq[u % 4] = add2(sq[u % 4], e);
         }
-#pragma unroll
-        for (int c = 0; c < C::P_COLS / 32; ++c)
-          tmem_st32(my_S + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+        static_assert(HN / 2 == 32, "a half's P is one store");
+        tmem_st32(my_S + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
         const float2 a2 = make_float2(alpha, alpha);
         l2 = fma2(l2, a2, add2(add2(sq[0], sq[1]), add2(sq[2], sq[3])));
         if (jj > 0 && __any_sync(full, resc)) {
           // S_j was issued after P V_{j-1} and is complete: O holds the sum up to there
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < D / 64; ++c) {
             uint32_t o[32];
             tmem_ld32(my_O + c * 32, o);
             tmem_wait_ld();
@@ -463,24 +497,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1) prefix_kernel(const _
         if (lane == 0) mbar_arrive(p_full(slot));
       }
       if (!alive) break;
-      if (!warp_wait(o_done(slot), ot & 1, abort_flag, p.status)) break;
+      float l = l2.x + l2.y, l_other;
+      if (!swap(l, &l_other) || !warp_wait(o_done(slot), ot & 1, abort_flag, p.status)) break;
       ++ot;
       tc_fence_after();
       const int rows = min(pl.slot_tokens, p.tokens - sg.tok0 - slot * pl.slot_tokens) * p.G;
       const long long row = sg.slot * (2 * kRows) + slot * kRows + r;
-      float* out = p.part_o + row * D;
+      float* out = p.part_o + row * D + half * (D / 2);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < D / 64; ++c) {
         uint32_t o[32];
         tmem_ld32(my_O + c * 32, o);
         tmem_wait_ld();
         if (r < rows) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(out + c * 32 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int e = 0; e < 32; e += 8) st_global32(out + c * 32 + e, &o[e]);
         }
       }
-      if (r < rows) p.part_ml[row] = make_float2(m_run, l2.x + l2.y);
+      if (half == 0 && r < rows) p.part_ml[row] = make_float2(m_run, l + l_other);
       tc_fence_before();
     }
   } else {
@@ -499,7 +533,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1) prefix_kernel(const _
           const int valid = p.len - j * kBN;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const int tok = half * 64 + (warp - 10) * 32 + lane;
+            const int tok = half * 64 + (warp - 18) * 32 + lane;
             const uint32_t src = sV + tv * C::TILE + tok * 128, dst = sH + th * C::VTILE + tok * 128;
 #pragma unroll
             for (int x = 0; x < 8; ++x) {   // 16 codes: 32 bytes of chunk x / 4
