@@ -67,7 +67,7 @@ struct DecodeParams {
   int prefix_pages, prefix_span;  // pages of the prefix, its length on the line
   int gang;                  // CTAs that walk together, each with another kv-head of the same pages
   int gangs, head_groups;    // ctas / gang, Hkv / gang
-  PrefixPlan pre;            // gangs > 0: prefix_kernel has run before this one; prt is 0 then
+  PrefixPlan pre;            // gangs > 0: the prefix is prefix_kernel's, behind this one; prt is 0 then
   uint32_t g_magic;          // ceil(2^32 / G): x / G = umulhi(x, g_magic) for G > 1 (see div_g)
 };
 
@@ -269,11 +269,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     tma_prefetch_map(&p.tk);
     tma_prefetch_map(&p.tv);
   }
-  // Nothing of the caller's, nor the workspace, is touched before the wait.  Behind
-  // prefix_kernel, which has made it, it comes last (see the end).
-  const bool behind = p.pre.gangs > 0;
-  if (!behind) pdl_wait();
-  pdl_trigger();  // not earlier: decode_finish reads the lengths before its own wait
+  pdl_wait();     // nothing of the caller's, nor the workspace, is touched before
+  pdl_trigger();  // not earlier: what follows relies on this wait (prefix_kernel, decode_finish)
   int* cum = reinterpret_cast<int*>(smem + C::OFF_CUM);
   const int run = line_places<kThreads>(p, cum, warp_sums, [&](int raw) {
     if (blockIdx.x == 0 && (raw < 0 || raw > a.max_kv_len)) atomicOr(a.status, kStatusBounds);
@@ -349,7 +346,6 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     if (!alive)  // let the copies already issued land before the CTA can exit
       for (uint32_t q = it > C::NST ? it - C::NST : 0; q < it; ++q)
         for (int spin = 0; spin < 1000000 && !mbar_try_wait(full(q % C::NST), (q / C::NST) & 1); ++spin) {}
-    if (behind) pdl_wait();
     return;
   }
 
@@ -557,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         };
         if (!edge) {
           pv(std::false_type{}, false, 0, true, true);
-        } else if (lim_lo == lim_hi || lim_lo >= s0 + 16 || lim_hi <= s0) {
+        } else if (lim_lo == lim_hi || lim_hi <= s0) {
           pv(std::false_type{}, true, lim_hi, true, true);
         } else {
           // The rows' limits differ inside these 16 tokens (drafted tokens): one product per
@@ -591,21 +587,20 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     const long long slot = static_cast<long long>(gang_no + was.unit) * p.gang + rank;
     // rounds of 4 rows x 128 columns (d 64: 8 rows x 64): few rows, few barriers
     constexpr int RPR = C::MROWS;
-#pragma unroll
-    for (int round = 0; round < kDecodeRows / RPR; ++round) {
-      if (round * RPR >= nrows) break;
-      const int half = round * RPR / 8;
+#pragma unroll 1
+    for (int round = 0; round * RPR < nrows; ++round) {
+      const bool upper = round * RPR >= 8;
       if (r0 / RPR == round % (8 / RPR)) {
         float* mine = merge + (warp * RPR + r0 % RPR) * C::MSTRIDE;
 #pragma unroll
         for (int x = 0; x < D / 8; x += 2) {
+          const float e0 = upper ? acc[x][2] : acc[x][0], e1 = upper ? acc[x][3] : acc[x][1];
+          const float f0 = upper ? acc[x + 1][2] : acc[x + 1][0], f1 = upper ? acc[x + 1][3] : acc[x + 1][1];
           if (FP8) {
-            *reinterpret_cast<float4*>(mine + x * 8 + qd * 4) = make_float4(
-                acc[x][2 * half], acc[x + 1][2 * half], acc[x][2 * half + 1], acc[x + 1][2 * half + 1]);
+            *reinterpret_cast<float4*>(mine + x * 8 + qd * 4) = make_float4(e0, f0, e1, f1);
           } else {
-            *reinterpret_cast<float2*>(mine + x * 8 + qd * 2) = make_float2(acc[x][2 * half], acc[x][2 * half + 1]);
-            *reinterpret_cast<float2*>(mine + x * 8 + 8 + qd * 2) =
-                make_float2(acc[x + 1][2 * half], acc[x + 1][2 * half + 1]);
+            *reinterpret_cast<float2*>(mine + x * 8 + qd * 2) = make_float2(e0, e1);
+            *reinterpret_cast<float2*>(mine + x * 8 + 8 + qd * 2) = make_float2(f0, f1);
           }
         }
       }
@@ -649,50 +644,49 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       consumer_sync();
     }
   }
-  // decode_finish waits for this kernel, which therefore does not end before prefix_kernel
-  if (behind) pdl_wait();
 }
 
-// The partials of one row: its (m, l) at ml[i * ml_step], its output at o[i * o_step].
+// The partials of one row: number i's (m, l) at ml[i * ml_step], its output at o[i * o_step].
 struct Pieces {
   const float2* ml;
   const float* o;
-  long long ml_step, o_step;
-  int n;
+  int ml_step, o_step, n;
 };
-// Pieces of a unit whose first tile lies at `first` on the line: CTA shares of `per`; its slots
-// start at (share + unit) * gang + rank, each of `rows` output rows.
+// Pieces of a unit whose tiles are first .. first + tiles - 1 on a line of which every CTA
+// takes `per`; its slots start at (share + unit) * gang + rank, each of `rows` output rows.
 __device__ __forceinline__ Pieces pieces_of(const float2* ml, const float* o, int ml_rows, int rows, int d, int first,
                                             int tiles, int unit, int gang, int rank, int per, int row) {
-  if (tiles == 0) return Pieces{nullptr, nullptr, 0, 0, 0};
-  const int c0 = first / per, c1 = (first + tiles - 1) / per;
+  const unsigned c0 = static_cast<unsigned>(first) / static_cast<unsigned>(per);
+  const unsigned c1 = static_cast<unsigned>(first + tiles - 1) / static_cast<unsigned>(per);
   const long long slot = static_cast<long long>(c0 + unit) * gang + rank;
-  return Pieces{ml + slot * ml_rows + row, o + (slot * rows + row) * d, static_cast<long long>(gang) * ml_rows,
-                static_cast<long long>(gang) * rows * d, c1 - c0 + 1};
+  return Pieces{ml + slot * ml_rows + row, o + (slot * rows + row) * d, gang * ml_rows, gang * rows * d,
+                tiles == 0 ? 0 : static_cast<int>(c1 - c0) + 1};
 }
-__device__ __forceinline__ Pieces own_pieces(const DecodeParams& p, int per, int b, int base, int pages, int kvh,
-                                             int rr) {
+// kvh = hg * gang + rank
+__device__ __forceinline__ Pieces own_pieces(const DecodeParams& p, int per, int b, int base, int pages, int hg,
+                                             int rank, int rr) {
   const DecodeArgs& a = p.a;
-  const int u = kvh / p.gang * p.rt + rr / kDecodeRows;
-  return pieces_of(a.part_ml, a.part_o, kDecodeRows, a.part_rows, a.d, base + u * span_of(pages) + kDecodeUnitCost,
-                   pages, p.head_groups * (p.prt + b * p.rt) + u, p.gang, kvh % p.gang, per, rr % kDecodeRows);
+  const int u = hg * p.rt + rr / kDecodeRows;
+  return pieces_of(a.part_ml, a.part_o, kDecodeRows, a.part_rows, a.d,
+                   base + u * (pages + kDecodeUnitCost) + kDecodeUnitCost, pages,
+                   p.head_groups * (p.prt + b * p.rt) + u, p.gang, rank, per, rr % kDecodeRows);
 }
-// row: (token of the batch) * G + q-head of the group
-__device__ __forceinline__ Pieces prefix_pieces(const DecodeParams& p, int per, int kvh, int row) {
+// tok: token of the batch; g: q-head of the group
+__device__ __forceinline__ Pieces prefix_pieces(const DecodeParams& p, int per, int hg, int rank, int tok, int g) {
   const DecodeArgs& a = p.a;
   const PrefixPlan& q = p.pre;
   if (q.gangs > 0) {
-    const int tok = row / a.G, pair = tok / (2 * q.slot_tokens), in = tok % (2 * q.slot_tokens);
-    const int u = kvh / q.gang * q.pairs + pair;
+    const unsigned tile = static_cast<unsigned>(tok) / static_cast<unsigned>(q.slot_tokens);
+    const int u = hg * q.pairs + static_cast<int>(tile / 2);
     return pieces_of(a.prefix_ml, a.prefix_o, 256, 256, a.d, u * (q.tiles + kPrefixUnitCost) + kPrefixUnitCost, q.tiles,
-                     u, q.gang, kvh % q.gang, q.per,
-                     in / q.slot_tokens * 128 + in % q.slot_tokens * a.G + row % a.G);
+                     u, q.gang, rank, q.per,
+                     static_cast<int>(tile % 2) * 128 + (tok - static_cast<int>(tile) * q.slot_tokens) * a.G + g);
   }
   if (p.prt == 0) return Pieces{nullptr, nullptr, 0, 0, 0};
-  const int u = kvh / p.gang * p.prt + row / kDecodeRows;
+  const int row = tok * a.G + g, u = hg * p.prt + row / kDecodeRows;
   return pieces_of(a.part_ml, a.part_o, kDecodeRows, a.part_rows, a.d,
-                   u * (p.prefix_pages + kDecodeUnitCost) + kDecodeUnitCost, p.prefix_pages, u, p.gang, kvh % p.gang,
-                   per, row % kDecodeRows);
+                   u * (p.prefix_pages + kDecodeUnitCost) + kDecodeUnitCost, p.prefix_pages, u, p.gang, rank, per,
+                   row % kDecodeRows);
 }
 // Pages of a sequence from its length on the line.
 __device__ __forceinline__ int pages_on_line(const DecodeParams& p, int length) {
@@ -718,12 +712,15 @@ struct RowPieces {
     return i < own.n ? own.ml[i * own.ml_step] : pre.ml[(i - own.n) * pre.ml_step];
   }
   __device__ __forceinline__ const float* out(int i) const {
-    return i < own.n ? own.o + i * own.o_step : pre.o + (i - own.n) * pre.o_step;
+    return i < own.n ? own.o + static_cast<long long>(i) * own.o_step
+                     : pre.o + static_cast<long long>(i - own.n) * pre.o_step;
   }
 };
 __device__ __forceinline__ RowPieces row_pieces(const DecodeParams& p, int per, int b, int base, int pages, int kvh,
-                                                int rr) {
-  return RowPieces{own_pieces(p, per, b, base, pages, kvh, rr), prefix_pieces(p, per, kvh, b * p.a.n * p.a.G + rr)};
+                                                int t, int g) {
+  const int hg = p.head_groups == 1 ? 0 : kvh / p.gang, rank = kvh - hg * p.gang;
+  return RowPieces{own_pieces(p, per, b, base, pages, hg, rank, t * p.a.G + g),
+                   prefix_pieces(p, per, hg, rank, b * p.a.n + t, g)};
 }
 
 // 2^(m - M), for a partial whose scores were all -inf 0 (and 1 where its sum is NaN: the
@@ -764,16 +761,16 @@ __device__ __forceinline__ void load_share(float (&x)[E], const float* src) {
 }
 
 // Joins the partials of rows whose keys fell to several CTAs (blocks below row_blocks, WPR
-// warps per row) and adds up the softmax weights (the other blocks, from the stored scores).
+// warps per row: 8, a block for one row, or 1) and adds up the softmax weights (the other blocks, from the stored scores).
 // What follows pdl_wait is latency, so where each row's partials lie is worked out before
-// it, from the lengths (decode_kernel triggers this launch after its own wait, when all that
+// it, from the lengths (decode_kernel triggers what follows after its own wait, when all that
 // came before it in the stream is complete), and all loads after it are independent.
 template <int D, bool SCORES, int WPR>
-__global__ void __launch_bounds__(kFinishThreads, SCORES ? 3 : 4) decode_finish(const __grid_constant__ DecodeParams p, int row_blocks) {
+__global__ void __launch_bounds__(kFinishThreads, 3) decode_finish(const __grid_constant__ DecodeParams p, int row_blocks) {
   const DecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, G = a.G, R = a.n * G;
   constexpr int E = D / 32, RPB = kFinishThreads / 32 / WPR;  // columns of a lane, rows of a block
-  constexpr int PF = WPR > 1 ? 8 : 4;                         // partials a warp loads at once
+  constexpr int PF = 8;                         // partials a warp loads at once
   __shared__ int cum[STEM_MAX_DECODE_SEQS + 1];
   __shared__ int sums[kFinishThreads / 32];
   __shared__ float lse2[256];
@@ -784,59 +781,63 @@ __global__ void __launch_bounds__(kFinishThreads, SCORES ? 3 : 4) decode_finish(
   const int per = max(1, (total + p.gangs - 1) / p.gangs);
 
   if (static_cast<int>(blockIdx.x) < row_blocks) {
-    const long long row = static_cast<long long>(blockIdx.x) * RPB + warp / WPR;  // token-major, then head
-    if (row >= static_cast<long long>(a.B) * a.n * a.Hq) return;                  // never with WPR = 8 (one row)
-    const int tok = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
-    const int b = tok / a.n, kvh = h / G, rr = (tok % a.n) * G + h % G;
-    const int base = cum[b], pages = pages_on_line(p, cum[b + 1] - base);
-    const RowPieces q = row_pieces(p, per, b, base, pages, kvh, rr);
-    const int n = q.count(), w = warp % WPR;
-    if (a.prefix_len == 0 && n == 1) return;  // written by the CTA that saw all of it
-    pdl_wait();
-    float x[PF][E];
-    float2 v[PF];
+    const int w = warp % WPR;
+    const unsigned rows = static_cast<unsigned>(a.B) * a.n * a.Hq;  // token-major, then head
+    bool waited = false;
+    for (unsigned row = blockIdx.x * RPB + warp / WPR; row < rows; row += row_blocks * RPB) {
+      const int tok = static_cast<int>(row / static_cast<unsigned>(a.Hq)), h = static_cast<int>(row) - tok * a.Hq;
+      const int b = a.n == 1 ? tok : tok / a.n, kvh = div_g(p, h), t = tok - b * a.n, g = h - kvh * G;
+      const int base = cum[b], pages = pages_on_line(p, cum[b + 1] - base);
+      const RowPieces q = row_pieces(p, per, b, base, pages, kvh, t, g);
+      const int n = q.count();
+      if (a.prefix_len == 0 && n == 1) continue;  // written by the CTA that saw all of it
+      if (!waited) pdl_wait();
+      waited = true;
+      float x[PF][E];
+      float2 v[PF];
 #pragma unroll
-    for (int k = 0; k < PF; ++k)
-      if (w + WPR * k < n) {
-        load_share(x[k], q.out(w + WPR * k) + lane * E);
-        v[k] = q.stats(w + WPR * k);
-      }
-    const float2 st = row_stats(q);
-    float o[E];
+      for (int k = 0; k < PF; ++k)
+        if (w + WPR * k < n) {
+          load_share(x[k], q.out(w + WPR * k) + lane * E);
+          v[k] = q.stats(w + WPR * k);
+        }
+      const float2 st = row_stats(q);
+      float o[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
+      for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll
-    for (int k = 0; k < PF; ++k)
-      if (w + WPR * k < n) {
-        const float f = piece_factor(v[k], st.x);
+      for (int k = 0; k < PF; ++k)
+        if (w + WPR * k < n) {
+          const float f = piece_factor(v[k], st.x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += f * x[k][e];
-      }
+          for (int e = 0; e < E; ++e) o[e] += f * x[k][e];
+        }
 #pragma unroll 4
-    for (int i = w + WPR * PF; i < n; i += WPR) {
-      load_share(x[0], q.out(i) + lane * E);
-      const float f = piece_factor(q.stats(i), st.x);
+      for (int i = w + WPR * PF; i < n; i += WPR) {
+        load_share(x[0], q.out(i) + lane * E);
+        const float f = piece_factor(q.stats(i), st.x);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += f * x[0][e];
+        for (int e = 0; e < E; ++e) o[e] += f * x[0][e];
+      }
+      if constexpr (WPR > 1) {  // one row a block, and one turn of the loop
+#pragma unroll
+        for (int e = 0; e < E; ++e) shares[tid * E + e] = o[e];
+        __syncthreads();
+        if (w != 0) return;
+#pragma unroll
+        for (int y = 1; y < WPR; ++y)
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] += shares[(tid + 32 * y) * E + e];
+      }
+      const float inv = st.x == -INFINITY && st.y == 0.f ? 0.f : a.v_scale / st.y;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.out) +
+                                                  ((static_cast<long long>(tok) * a.Hq + h) * D + lane * E) * 2);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+      if (a.lse != nullptr && lane == 0)
+        a.lse[static_cast<long long>(h) * a.B * a.n + tok] =
+            st.y == 0.f ? -INFINITY : (st.x + log2f(st.y)) * 0.69314718055994531f;
     }
-    if constexpr (WPR > 1) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) shares[tid * E + e] = o[e];
-      __syncthreads();
-      if (w != 0) return;
-#pragma unroll
-      for (int y = 1; y < WPR; ++y)
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += shares[(tid + 32 * y) * E + e];
-    }
-    const float inv = st.x == -INFINITY && st.y == 0.f ? 0.f : a.v_scale / st.y;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.out) +
-                                                ((static_cast<long long>(tok) * a.Hq + h) * D + lane * E) * 2);
-#pragma unroll
-    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-    if (a.lse != nullptr && lane == 0)
-      a.lse[static_cast<long long>(h) * a.B * a.n + tok] =
-          st.y == 0.f ? -INFINITY : (st.x + log2f(st.y)) * 0.69314718055994531f;
     return;
   }
 
@@ -888,7 +889,7 @@ __global__ void __launch_bounds__(kFinishThreads, SCORES ? 3 : 4) decode_finish(
         for (int r = 0; r < 4; ++r)
           if (r < nr && j < len) x[r] = *reinterpret_cast<const float4*>(sc + r * a.score_stride);
         for (int r = warp; r < nr; r += kFinishThreads / 32) {
-          const float2 st = row_stats(row_pieces(p, per, b, base, pages, kvh, r0 + r));
+          const float2 st = row_stats(row_pieces(p, per, b, base, pages, kvh, div_g(p, r0 + r), r0 + r - div_g(p, r0 + r) * G));
           // a row that sees nothing adds exp2(-inf - inf) = 0
           if (lane == 0) lse2[r] = st.y == 0.f ? INFINITY : st.x + log2f(st.y);
         }
@@ -922,6 +923,8 @@ cudaError_t run(const DecodeParams& prm, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_dependent(decode_kernel<D, FP8, SCORES>, prm.gangs * prm.gang, kThreads, C::SMEM, 1, st, prm);
   if (e != cudaSuccess) return e;
+  // behind it, so that its partials, the larger ones, are the last into L2
+  if (prm.pre.gangs > 0 && (e = launch_prefix(prm.a, prm.pre, FP8, st)) != cudaSuccess) return e;
   const DecodeArgs& a = prm.a;
   const long long rows = static_cast<long long>(a.B) * a.n * a.Hq;
   const long long chunks =
@@ -932,7 +935,8 @@ cudaError_t run(const DecodeParams& prm, cudaStream_t st) {
   if (rows <= kDecodeCtas)
     return launch_dependent(decode_finish<D, SCORES, 8>, static_cast<int>(rows) + weight_blocks, kFinishThreads, 0, 1,
                             st, prm, static_cast<int>(rows));
-  const int row_blocks = static_cast<int>((rows + 7) / 8);
+  constexpr int kResident = 3 * kDecodeCtas / 2;  // blocks at a time: each plans once
+  const int row_blocks = static_cast<int>((rows + 7) / 8 < kResident ? (rows + 7) / 8 : kResident);
   return launch_dependent(decode_finish<D, SCORES, 1>, row_blocks + weight_blocks, kFinishThreads, 0, 1, st, prm,
                           row_blocks);
 }
@@ -966,7 +970,6 @@ cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st) {
   prm.gangs = (2 * sms < kDecodeCtas ? 2 * sms : kDecodeCtas) / prm.gang;
   if (bound < prm.gangs) prm.gangs = static_cast<int>(bound);
   const bool scores = a.scores != nullptr;
-  if (prm.pre.gangs > 0 && (e = launch_prefix(a, prm.pre, fp8, st)) != cudaSuccess) return e;
   if (fp8) return scores ? run<128, true, true>(prm, st) : run<128, true, false>(prm, st);
   if (a.d == 128) return scores ? run<128, false, true>(prm, st) : run<128, false, false>(prm, st);
   return scores ? run<64, false, true>(prm, st) : run<64, false, false>(prm, st);

@@ -219,8 +219,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1) prefix_kernel(const _
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();
-  pdl_trigger();  // decode_kernel starts where CTAs of this one end, and waits for it at its own end
+  // Launched behind decode_kernel, this one starts where CTAs of that one end: it needs
+  // nothing of it, and what came before it was complete when its CTAs let this launch go.
+  pdl_trigger();
   const PrefixPlan& pl = p.plan;
   const int gang_no = static_cast<int>(blockIdx.x) / pl.gang, rank = static_cast<int>(blockIdx.x) % pl.gang;
   const int total = pl.head_groups * pl.pairs * (pl.tiles + kPrefixUnitCost);
@@ -562,6 +563,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1) prefix_kernel(const _
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  pdl_wait();  // decode_finish waits for this kernel, which therefore does not end before decode_kernel
 }
 
 template <int D, bool FP8>

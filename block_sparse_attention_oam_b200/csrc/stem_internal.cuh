@@ -474,7 +474,7 @@ constexpr int kDecodeCtas = 296;      // two on each of 148 SMs
 constexpr int kDecodeRows = 16;       // query rows of a unit
 // What a unit costs beside its tiles (loading Q, joining the warps), in tiles: it counts as
 // that many empty ones on the line, so that a CTA with many short sequences gets fewer.
-constexpr int kDecodeUnitCost = 2;
+constexpr int kDecodeUnitCost = 4;
 
 // The kv-heads that CTAs walk side by side: neighbours in memory (a page of one head is 64
 // pieces of 128 or 256 bytes), so that they read whole DRAM rows between them.
