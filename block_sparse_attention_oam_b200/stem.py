@@ -411,7 +411,7 @@ def _dtype_code(name: str) -> int:
 
 def _tensor(name: str, t, shape, dtype, device):
     """Address of a dense tensor of this shape (None: any length), type and device."""
-    if t.dtype == dtype and t.device == device and t.is_contiguous():
+    if t.dtype is dtype and t.device == device and t.is_contiguous():
         got = t.shape
         if got == shape or (len(got) == len(shape) and all(w is None or w == g for w, g in zip(shape, got))):
             return t.data_ptr()
@@ -427,14 +427,18 @@ def _pages(name: str, c: PagedKV, num_seqs: int, Hkv: int, d: int, dtype, device
                   _tensor(f"{name}.block_table", table, (num_seqs, width), torch.int32, device), PAGE_SIZE, width, slots)
 
 
-def _call_on(device, stream, fn, *args) -> None:
-    """Call the library on the tensors' device, on `stream` or that device's current one."""
-    s = torch.cuda.current_stream(device) if stream is None else stream
+def _raw(stream, device) -> int:
+    """The stream's handle, or that of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _call_on(device, fn, *args) -> None:
+    """Call the library with the tensors' device current."""
     if device.index == torch.cuda.current_device():
-        status = fn(*args, s.cuda_stream)
+        status = fn(*args)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, s.cuda_stream)
+            status = fn(*args)
     if status != STEM_OK:
         _check(status)
 
@@ -459,17 +463,22 @@ def stem_decode(dec: Decode, q, cache: PagedKV, kv_lens, prefix_table=None, weig
         ws = decode_workspace(dec, dev)
     if dec.weights != (weights_out is not None) or (weights_in is not None and weights_out is None):
         raise ValueError("weights_out goes with Decode(weights=True), weights_in with weights_out")
-    stride = weights_out.shape[-1] if dec.weights else 0
-    ok = torch.float32
-    _call_on(dev, stream, lib().stem_decode, dec.c, _tensor("q", q, (B * n, Hq, d), dec._torch, dev),
-             _pages("cache", cache, B, Hkv, d, dec._torch, dev), _tensor("kv_lens", kv_lens, (B,), torch.int32, dev),
-             None if prefix_table is None else _tensor("prefix_table", prefix_table, (-(-dec.prefix_len // PAGE_SIZE),),
-                                                       torch.int32, dev),
-             None if weights_in is None else _tensor("weights_in", weights_in, (B, Hkv, stride), ok, dev),
-             None if weights_out is None else _tensor("weights_out", weights_out, (B, Hkv, stride), ok, dev), stride,
-             _tensor("out", out, (B * n, Hq, d), torch.bfloat16, dev),
-             None if lse is None else _tensor("lse", lse, (Hq, B * n), ok, dev),
-             _tensor("ws", ws, (None,), torch.uint8, dev), ws.numel())
+    i32, f32, stride, prefix = torch.int32, torch.float32, 0, None
+    if prefix_table is not None:
+        prefix = _tensor("prefix_table", prefix_table, (-(-dec.prefix_len // PAGE_SIZE),), i32, dev)
+    w_in = w_out = None
+    if weights_out is not None:
+        stride = weights_out.shape[-1]
+        w_out = _tensor("weights_out", weights_out, (B, Hkv, stride), f32, dev)
+        if weights_in is not None:
+            w_in = _tensor("weights_in", weights_in, (B, Hkv, stride), f32, dev)
+    T = B * n
+    size = ws.numel()
+    _call_on(dev, lib().stem_decode, dec.c, _tensor("q", q, (T, Hq, d), dec._torch, dev),
+             _pages("cache", cache, B, Hkv, d, dec._torch, dev), _tensor("kv_lens", kv_lens, (B,), i32, dev), prefix,
+             w_in, w_out, stride, _tensor("out", out, (T, Hq, d), torch.bfloat16, dev),
+             None if lse is None else _tensor("lse", lse, (Hq, T), f32, dev),
+             _tensor("ws", ws, (size,), torch.uint8, dev), size, _raw(stream, dev))
     return out
 
 
@@ -522,14 +531,16 @@ def stem_evict(ev: Evict, src: PagedKV, kv_lens, weights, dst: PagedKV, kv_lens_
         keep = torch.empty((B, Hkv, ev.budget), dtype=torch.int32, device=dev)
     if ws is None:
         ws = evict_workspace(ev, dev)
-    _call_on(dev, stream, lib().stem_evict, ev.c, _pages("src", src, B, Hkv, d, ev._torch, dev),
-             _tensor("kv_lens", kv_lens, (B,), torch.int32, dev), _tensor("weights", weights, (B, Hkv, None), f32, dev),
-             weights.shape[-1], _pages("dst", dst, B, Hkv, d, ev._torch, dev),
-             _tensor("kv_lens_out", kv_lens_out, (B,), torch.int32, dev),
-             None if weights_out is None else _tensor("weights_out", weights_out, (B, Hkv, None), f32, dev),
-             0 if weights_out is None else weights_out.shape[-1],
-             _tensor("keep", keep, (B, Hkv, ev.budget), torch.int32, dev), _tensor("ws", ws, (None,), torch.uint8, dev),
-             ws.numel())
+    i32, stride, size = torch.int32, weights.shape[-1], ws.numel()
+    w_out, out_stride = None, 0
+    if weights_out is not None:
+        out_stride = weights_out.shape[-1]
+        w_out = _tensor("weights_out", weights_out, (B, Hkv, out_stride), f32, dev)
+    _call_on(dev, lib().stem_evict, ev.c, _pages("src", src, B, Hkv, d, ev._torch, dev),
+             _tensor("kv_lens", kv_lens, (B,), i32, dev), _tensor("weights", weights, (B, Hkv, stride), f32, dev), stride,
+             _pages("dst", dst, B, Hkv, d, ev._torch, dev), _tensor("kv_lens_out", kv_lens_out, (B,), i32, dev), w_out,
+             out_stride, _tensor("keep", keep, (B, Hkv, ev.budget), i32, dev),
+             _tensor("ws", ws, (size,), torch.uint8, dev), size, _raw(stream, dev))
     return keep, kv_lens_out
 
 
