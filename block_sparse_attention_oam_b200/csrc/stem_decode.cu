@@ -842,9 +842,10 @@ __global__ void __launch_bounds__(kFinishThreads, 3) decode_finish(const __grid_
   }
 
   if constexpr (SCORES) {
-    // Chunks of 1024 tokens (4 per thread) of all (sequence, kv-head) pairs, dealt round robin.
+    // Chunks of 1024 tokens (4 per thread) of all (sequence, kv-head) pairs, an equal share per
+    // block: a pair's log-sum-exps are worked out once, then its chunks go without a barrier.
     __shared__ int chunk_cum[STEM_MAX_DECODE_SEQS + 1];
-    constexpr int kChunk = kFinishThreads * 4 / kTile;  // pages
+    constexpr int kSpan = kFinishThreads * 4, kChunk = kSpan / kTile;  // tokens, pages
     if (warp == 0) {
       int run = 0;
       for (int b0 = 0; b0 < a.B; b0 += 32) {
@@ -862,56 +863,54 @@ __global__ void __launch_bounds__(kFinishThreads, 3) decode_finish(const __grid_
       if (lane == 0) chunk_cum[a.B] = run;
     }
     __syncthreads();
-    const int chunks = chunk_cum[a.B], nb = gridDim.x - row_blocks;
+    const int chunks = chunk_cum[a.B], nb = gridDim.x - row_blocks, share = (chunks + nb - 1) / nb;
+    int c = min(chunks, static_cast<int>(blockIdx.x - row_blocks) * share);
+    const int end = min(chunks, c + share);
     bool waited = false;
-    for (int c = blockIdx.x - row_blocks; c < chunks; c += nb) {
+    while (c < end) {
       for (int b = tid; b < a.B; b += kFinishThreads)
         if (chunk_cum[b] <= c && c < chunk_cum[b + 1]) where = b;
       __syncthreads();
       const int b = where;
       const int base = cum[b], pages = pages_on_line(p, cum[b + 1] - base);
       const int off = c - chunk_cum[b], each = (pages + kChunk - 1) / kChunk, kvh = off / each;
-      const int len = clamp_len(a, b), j = (off % each) * (kFinishThreads * 4) + tid * 4;
+      const int k0 = off - kvh * each, k1 = min(each, k0 + (end - c)), len = clamp_len(a, b);
+      c += k1 - k0;
       const long long unit = static_cast<long long>(b) * a.Hkv + kvh;
       const float* win = a.weights_in ? a.weights_in + unit * a.weights_stride : nullptr;
       float* wout = a.weights_out + unit * a.weights_stride;
       if (!waited) pdl_wait();
       waited = true;
-      float sum[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] = win && j + e < len ? win[j + e] : 0.f;
-      float add[4] = {0.f, 0.f, 0.f, 0.f};
       for (int r0 = 0; r0 < R; r0 += 256) {
         const int nr = min(256, R - r0);
-        const float* sc = a.scores + (unit * R + r0) * a.score_stride + j;
-        float4 x[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (r < nr && j < len) x[r] = *reinterpret_cast<const float4*>(sc + r * a.score_stride);
         for (int r = warp; r < nr; r += kFinishThreads / 32) {
-          const float2 st = row_stats(row_pieces(p, per, b, base, pages, kvh, div_g(p, r0 + r), r0 + r - div_g(p, r0 + r) * G));
+          const int t = div_g(p, r0 + r);
+          const float2 st = row_stats(row_pieces(p, per, b, base, pages, kvh, t, r0 + r - t * G));
           // a row that sees nothing adds exp2(-inf - inf) = 0
           if (lane == 0) lse2[r] = st.y == 0.f ? INFINITY : st.x + log2f(st.y);
         }
         __syncthreads();
-        auto take = [&](const float4& y, float l) {
-          add[0] += ex2_approx(y.x - l);
-          add[1] += ex2_approx(y.y - l);
-          add[2] += ex2_approx(y.z - l);
-          add[3] += ex2_approx(y.w - l);
-        };
-        if (j < len) {
+        const float* was = r0 > 0 ? wout : win;
+        for (int j = k0 * kSpan + tid * 4; j < min(len, k1 * kSpan); j += kSpan) {
+          const float* sc = a.scores + (unit * R + r0) * a.score_stride + j;
+          float sum[4], add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (r < nr) take(x[r], lse2[r]);
+          for (int e = 0; e < 4; ++e) sum[e] = was && j + e < len ? was[j + e] : 0.f;
 #pragma unroll 4
-          for (int r = 4; r < nr; ++r) take(*reinterpret_cast<const float4*>(sc + r * a.score_stride), lse2[r]);
+          for (int r = 0; r < nr; ++r) {
+            const float4 x = *reinterpret_cast<const float4*>(sc + r * a.score_stride);
+            const float l = lse2[r];
+            add[0] += ex2_approx(x.x - l);
+            add[1] += ex2_approx(x.y - l);
+            add[2] += ex2_approx(x.z - l);
+            add[3] += ex2_approx(x.w - l);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + e < len) wout[j + e] = sum[e] + add[e];
         }
         __syncthreads();
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (j + e < len) wout[j + e] = sum[e] + add[e];
     }
   }
 }
@@ -929,14 +928,19 @@ cudaError_t run(const DecodeParams& prm, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.B) * a.n * a.Hq;
   const long long chunks =
       static_cast<long long>(a.B) * a.Hkv * ((a.max_kv_len + kFinishThreads * 4 - 1) / (kFinishThreads * 4));
-  const int weight_blocks = SCORES ? static_cast<int>(chunks < 3 * kDecodeCtas ? chunks : 3 * kDecodeCtas) : 0;
+  // As many blocks as are resident at once (three per SM), so that each plans once, ahead of
+  // the wait, and then takes row after row or chunk after chunk.
+  constexpr int kResident = 3 * kDecodeCtas / 2;
   // Few rows have many partials each (their tiles are spread over all CTAs): a block per row
   // then, else a warp per row.
-  if (rows <= kDecodeCtas)
-    return launch_dependent(decode_finish<D, SCORES, 8>, static_cast<int>(rows) + weight_blocks, kFinishThreads, 0, 1,
-                            st, prm, static_cast<int>(rows));
-  constexpr int kResident = 3 * kDecodeCtas / 2;  // blocks at a time: each plans once
-  const int row_blocks = static_cast<int>((rows + 7) / 8 < kResident ? (rows + 7) / 8 : kResident);
+  const bool few = rows <= kDecodeCtas;
+  const long long most = few ? rows : (SCORES ? kResident / 4 : kResident);
+  const int row_blocks = static_cast<int>(few || (rows + 7) / 8 > most ? most : (rows + 7) / 8);
+  const int left = row_blocks < kResident - 32 ? kResident - row_blocks : 32;
+  const int weight_blocks = SCORES ? static_cast<int>(chunks < left ? chunks : left) : 0;
+  if (few)
+    return launch_dependent(decode_finish<D, SCORES, 8>, row_blocks + weight_blocks, kFinishThreads, 0, 1, st, prm,
+                            row_blocks);
   return launch_dependent(decode_finish<D, SCORES, 1>, row_blocks + weight_blocks, kFinishThreads, 0, 1, st, prm,
                           row_blocks);
 }
