@@ -47,17 +47,24 @@ struct Cfg {
   static constexpr int CHUNK = kTile * 128;         // one box: 64 tokens of 128 bytes
   static constexpr int TILE = kTile * D * ES;
   static constexpr int STAGE = 2 * TILE;            // K and V
-  static constexpr int NST = 96 * 1024 / STAGE;
+  // Two CTAs per SM where a tile is 32 KB, three where it is 16 KB: the same bytes in flight,
+  // and per byte twice the work, which is latency and wants more warps
+  static constexpr int CTAS = STAGE == 32 * 1024 ? 2 : 3;
+  static constexpr int NST = 3;
   static constexpr int MROWS = 512 / D;             // rows joined in one round
   static constexpr int MSTRIDE = D + 8;             // floats: the rows' banks apart
   static constexpr int MERGE = 4 * MROWS * MSTRIDE * 4;  // of four warps
   static constexpr int OFF_MERGE = NST * STAGE;
   static constexpr int OFF_ML = OFF_MERGE + MERGE;  // float2 [4][16]
   static constexpr int OFF_BAR = OFF_ML + 512;
-  static constexpr int OFF_CUM = OFF_BAR + 512;     // the line: int [STEM_MAX_DECODE_SEQS + 1]
+  static constexpr int QSTRIDE = D * 2 + 16;        // a Q row in 16 bits; the rows' banks apart
+  static constexpr bool Q_IN_MERGE = CTAS == 2;     // no room of its own: a barrier before the joining
+  static constexpr int OFF_Q = Q_IN_MERGE ? OFF_MERGE : OFF_BAR + 512;
+  static constexpr int QPIECES = D * ES / 128;      // 16-byte pieces of the unit's Q a thread loads
+  static constexpr int OFF_CUM = OFF_BAR + 512 + (Q_IN_MERGE ? 0 : kDecodeRows * QSTRIDE);  // the line: int [STEM_MAX_DECODE_SEQS + 1]
   static constexpr int SMEM = OFF_CUM + (STEM_MAX_DECODE_SEQS + 1) * 4 + 1024;  // 1024: alignment
   static_assert(DCH >= 1 && NST >= 3 && NST <= 16, "ring");
-  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "resident CTAs");
 };
 
 struct DecodeParams {
@@ -192,10 +199,10 @@ struct Walk {
   }
 };
 
-// A 4-byte load that stays where it is written (before the barriers that follow).
-__device__ __forceinline__ uint32_t ld_early(const void* at) {
-  uint32_t r;
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(r) : "l"(at));
+// A load that stays where it is written (before the barriers that follow).
+__device__ __forceinline__ uint4 ld_early(const uint4* at) {
+  uint4 r;
+  asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(at));
   return r;
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -242,7 +249,7 @@ __device__ __forceinline__ uint32_t keep_below(int j, int limit) {
 }
 
 template <int D, bool FP8, bool SCORES>
-__global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) decode_kernel(const __grid_constant__ DecodeParams p) {
   using C = Cfg<D, FP8>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem =
@@ -357,32 +364,49 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
   const uint32_t v_row = static_cast<uint32_t>(warp * 16 + (mi & 1) * 8 + (lane & 7)) * 128;
   const int k_sub = FP8 ? mi >> 1 : mi & 1, v_sub = mi >> 1;
   const int sw = lane & 7;
-  // Q fragments of a unit's rows
-  uint32_t qf[D / 16][4];
+  // A unit's Q, 16 rows in 16 bits, lies in shared memory: as fragments it took 32 registers.
+  // FP8: in the order in which e4m3x2_to_h2 gives K's codes, a word's low pairs of a group of
+  // 16, then its high pairs.
+  unsigned char* sq = smem + C::OFF_Q;
+  const uint32_t q_frag = smem_u32(sq) + ((lane & 7) + (mi & 1) * 8) * C::QSTRIDE + (mi >> 1) * 16;
+  constexpr int PPR = D * C::ES / 16;  // pieces of a row
+  uint4 qn[C::QPIECES];
   auto load_q = [&](const Seg& g) {
     const int first = g.rtile * kDecodeRows;
     const int nrows = min(kDecodeRows, (g.own ? a.n * G : a.B * a.n * G) - first);
-    const unsigned char* qb = static_cast<const unsigned char*>(a.q);
-    const int g0 = (g.own ? g.b * a.n * G : 0) + first + r0, g1 = g0 + 8;
-    const int k0 = div_g(p, g0), k1 = div_g(p, g1);
-    const unsigned char* q0 = qb + (static_cast<long long>(k0) * a.Hq + g.kvh * G + g0 - k0 * G) * (D * C::ES) + qd * 4;
-    const unsigned char* q1 = qb + (static_cast<long long>(k1) * a.Hq + g.kvh * G + g1 - k1 * G) * (D * C::ES) + qd * 4;
-    const bool on0 = r0 < nrows, on1 = r0 + 8 < nrows;
-    constexpr int STEP = FP8 ? 16 : 32;
+    const int base = (g.own ? g.b * a.n * G : 0) + first;
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      qf[k][0] = on0 ? ld_early(q0 + k * STEP) : 0u;
-      qf[k][1] = on1 ? ld_early(q1 + k * STEP) : 0u;
-      if (!FP8) {
-        qf[k][2] = on0 ? ld_early(q0 + k * STEP + 16) : 0u;
-        qf[k][3] = on1 ? ld_early(q1 + k * STEP + 16) : 0u;
+    for (int k = 0; k < C::QPIECES; ++k) {
+      const int x = tid + 128 * k, r = x / PPR, row = base + r, tok = div_g(p, row);
+      const long long at = (static_cast<long long>(tok) * a.Hq + g.kvh * G + row - tok * G) * PPR + x % PPR;
+      qn[k] = make_uint4(0, 0, 0, 0);
+      if (r < nrows) qn[k] = ld_early(static_cast<const uint4*>(a.q) + at);
+    }
+  };
+  auto store_q = [&]() {
+#pragma unroll
+    for (int k = 0; k < C::QPIECES; ++k) {
+      const int x = tid + 128 * k;
+      unsigned char* to = sq + x / PPR * C::QSTRIDE + x % PPR * (FP8 ? 32 : 16);
+      if (FP8) {
+        const uint4 v = qn[k];
+        *reinterpret_cast<uint4*>(to) = make_uint4(e4m3x2_to_h2(v.x & 0xFFFFu), e4m3x2_to_h2(v.y & 0xFFFFu),
+                                                   e4m3x2_to_h2(v.z & 0xFFFFu), e4m3x2_to_h2(v.w & 0xFFFFu));
+        *reinterpret_cast<uint4*>(to + 16) =
+            make_uint4(e4m3x2_to_h2(v.x >> 16), e4m3x2_to_h2(v.y >> 16), e4m3x2_to_h2(v.z >> 16), e4m3x2_to_h2(v.w >> 16));
+      } else {
+        *reinterpret_cast<uint4*>(to) = qn[k];
       }
     }
+    consumer_sync();
   };
   Walk walk{t0, t1, 0, rank, -1, 0, 0};
   Seg sg;
   bool have = walk.next(p, cum, &sg);
-  if (have) load_q(sg);
+  if (have) {
+    load_q(sg);
+    store_q();
+  }
   uint32_t it = 0;
   while (have) {
     const int rows_all = sg.own ? a.n * G : a.B * a.n * G;
@@ -396,16 +420,6 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     };
     const int lim_lo = limit_of(0), lim_hi = limit_of(nrows - 1);
     const int lim0 = limit_of(min(r0, nrows - 1)), lim1 = limit_of(min(r0 + 8, nrows - 1));
-    if (FP8) {  // four codes a word: the k positions 2 qd, + 1 and 2 qd + 8, + 9 of the fragment
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t x = qf[k][0], y = qf[k][1];
-        qf[k][0] = e4m3x2_to_h2(x & 0xFFFFu);
-        qf[k][2] = e4m3x2_to_h2(x >> 16);
-        qf[k][1] = e4m3x2_to_h2(y & 0xFFFFu);
-        qf[k][3] = e4m3x2_to_h2(y >> 16);
-      }
-    }
     float* srow = nullptr;
     if (SCORES && sg.own)
       srow = a.scores + (static_cast<long long>(sg.b * a.Hkv + sg.kvh) * rows_all + first) * a.score_stride;
@@ -431,22 +445,25 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
         if (FP8) {
 #pragma unroll
           for (int k = 0; k < D / 16; k += 2) {
-            uint32_t r[4];
+            uint32_t r[4], q[2][4];
             ldsm4(r, kt + k_row + (((k + k_sub) ^ sw) << 4));
+            ldsm4(q[0], q_frag + k * 32);
+            ldsm4(q[1], q_frag + k * 32 + 32);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                mma16816<true>(kk ? s_odd[j] : s[j], qf[k + kk], e4m3x2_to_h2(r[2 * kk + j] & 0xFFFFu), e4m3x2_to_h2(r[2 * kk + j] >> 16));
+                mma16816<true>(kk ? s_odd[j] : s[j], q[kk], e4m3x2_to_h2(r[2 * kk + j] & 0xFFFFu), e4m3x2_to_h2(r[2 * kk + j] >> 16));
           }
         } else {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const int c = 2 * k + k_sub;
-            uint32_t r[4];
+            uint32_t r[4], q[4];
             ldsm4(r, kt + (c >> 3) * C::CHUNK + k_row + (((c & 7) ^ sw) << 4));
-            mma16816<false>(k & 1 ? s_odd[0] : s[0], qf[k], r[0], r[1]);
-            mma16816<false>(k & 1 ? s_odd[1] : s[1], qf[k], r[2], r[3]);
+            ldsm4(q, q_frag + k * 32);
+            mma16816<false>(k & 1 ? s_odd[0] : s[0], q, r[0], r[1]);
+            mma16816<false>(k & 1 ? s_odd[1] : s[1], q, r[2], r[3]);
           }
         }
 #pragma unroll
@@ -575,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
     if (have) load_q(sg);
 
     // join the four warps' shares
+    if (C::Q_IN_MERGE) consumer_sync();
     l0 += __shfl_xor_sync(all, l0, 1);
     l1 += __shfl_xor_sync(all, l1, 1);
     l0 += __shfl_xor_sync(all, l0, 2);
@@ -643,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const __grid_consta
       }
       consumer_sync();
     }
+    if (have) store_q();
   }
 }
 
@@ -930,10 +949,10 @@ cudaError_t run(const DecodeParams& prm, cudaStream_t st) {
       static_cast<long long>(a.B) * a.Hkv * ((a.max_kv_len + kFinishThreads * 4 - 1) / (kFinishThreads * 4));
   // As many blocks as are resident at once (three per SM), so that each plans once, ahead of
   // the wait, and then takes row after row or chunk after chunk.
-  constexpr int kResident = 3 * kDecodeCtas / 2;
+  constexpr int kResident = 3 * kDecodeSms;
   // Few rows have many partials each (their tiles are spread over all CTAs): a block per row
   // then, else a warp per row.
-  const bool few = rows <= kDecodeCtas;
+  const bool few = rows <= 2 * kDecodeSms;
   const long long most = few ? rows : (SCORES ? kResident / 4 : kResident);
   const int row_blocks = static_cast<int>(few || (rows + 7) / 8 > most ? most : (rows + 7) / 8);
   const int left = row_blocks < kResident - 32 ? kResident - row_blocks : 32;
@@ -971,7 +990,8 @@ cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st) {
   const long long bound = static_cast<long long>(prm.head_groups) *
                           (prm.prt * prm.prefix_pages +
                            static_cast<long long>(a.B) * prm.rt * ((a.max_kv_len + kTile - 1) / kTile));
-  prm.gangs = (2 * sms < kDecodeCtas ? 2 * sms : kDecodeCtas) / prm.gang;
+  const int resident = (fp8 || a.d == 64 ? 3 : 2) * (sms < kDecodeSms ? sms : kDecodeSms);  // Cfg::CTAS per SM
+  prm.gangs = resident / prm.gang;
   if (bound < prm.gangs) prm.gangs = static_cast<int>(bound);
   const bool scores = a.scores != nullptr;
   if (fp8) return scores ? run<128, true, true>(prm, st) : run<128, true, false>(prm, st);

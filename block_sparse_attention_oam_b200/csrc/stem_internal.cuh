@@ -470,7 +470,8 @@ bool make_map_rows(CUtensorMap* m, const void* ptr, bool fp8, int d, int G, int 
 // the prefix's units (head group, 16-row tile of all sequences' rows), then sequence after
 // sequence its own (head group, 16-row tile) units; every unit is as many tiles as its keys
 // have pages, and the CTAs take equal shares of the line (see stem_decode.cu).
-constexpr int kDecodeCtas = 296;      // two on each of 148 SMs
+constexpr int kDecodeSms = 148;
+constexpr int kDecodeCtas = 3 * kDecodeSms;  // at most
 constexpr int kDecodeRows = 16;       // query rows of a unit
 // What a unit costs beside its tiles (loading Q, joining the warps), in tiles: it counts as
 // that many empty ones on the line, so that a CTA with many short sequences gets fewer.
