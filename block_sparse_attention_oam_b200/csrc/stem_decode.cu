@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) decode_kernel(con
       if (!sg.own) return sg.len;
       return max(0, sg.len - a.n + div_g(p, first + r) + 1);
     };
+    const bool upper_rows = nrows > 8;
     const int lim_lo = limit_of(0), lim_hi = limit_of(nrows - 1);
     const int lim0 = limit_of(min(r0, nrows - 1)), lim1 = limit_of(min(r0 + 8, nrows - 1));
     float* srow = nullptr;
@@ -487,13 +488,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) decode_kernel(con
               *reinterpret_cast<float2*>(at + (r0 + 8) * a.score_stride) = make_float2(s[j][2], s[j][3]);
           }
         }
-        // running maximum (raised lazily, when it grows by more than 2^8: p <= 2^8 until then)
-        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        // running maximum (raised lazily, when it grows by more than 2^8: p <= 2^8 until then);
+        // the upper eight rows only where the unit has them
+        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])), x1 = -INFINITY;
         x0 = fmaxf(x0, __shfl_xor_sync(all, x0, 1));
-        x1 = fmaxf(x1, __shfl_xor_sync(all, x1, 1));
         x0 = fmaxf(x0, __shfl_xor_sync(all, x0, 2));
-        x1 = fmaxf(x1, __shfl_xor_sync(all, x1, 2));
+        if (upper_rows) {
+          x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+          x1 = fmaxf(x1, __shfl_xor_sync(all, x1, 1));
+          x1 = fmaxf(x1, __shfl_xor_sync(all, x1, 2));
+        }
         if (__any_sync(all, x0 > m0 + 8.0f || x1 > m1 + 8.0f)) {
           const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
           const float a0 = n0 == m0 ? 1.0f : ex2_approx(m0 - n0), a1 = n1 == m1 ? 1.0f : ex2_approx(m1 - n1);
@@ -509,16 +513,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) decode_kernel(con
             acc[i][3] *= a1;
           }
         }
-        const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+        const float u0 = m0 == -INFINITY ? 0.f : m0;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           s[j][0] = ex2_approx(s[j][0] - u0);
           s[j][1] = ex2_approx(s[j][1] - u0);
-          s[j][2] = ex2_approx(s[j][2] - u1);
-          s[j][3] = ex2_approx(s[j][3] - u1);
         }
         l0 += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
-        l1 += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
+        if (upper_rows) {
+          const float u1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            s[j][2] = ex2_approx(s[j][2] - u1);
+            s[j][3] = ex2_approx(s[j][3] - u1);
+          }
+          l1 += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
+        } else {
+          s[0][2] = s[0][3] = s[1][2] = s[1][3] = 0.f;
+        }
         uint32_t pf[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
