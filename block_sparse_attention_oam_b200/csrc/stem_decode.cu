@@ -795,7 +795,9 @@ __device__ __forceinline__ void load_share(float (&x)[E], const float* src) {
 // warps per row: 8, a block for one row, or 1) and adds up the softmax weights (the other blocks, from the stored scores).
 // What follows pdl_wait is latency, so where each row's partials lie is worked out before
 // it, from the lengths (decode_kernel triggers what follows after its own wait, when all that
-// came before it in the stream is complete), and all loads after it are independent.
+// came before it in the stream is complete), and all loads after it are independent.  Every
+// block waits, those with nothing to join too: what follows in the stream takes this launch's
+// end for decode_kernel's.
 template <int D, bool SCORES, int WPR>
 __global__ void __launch_bounds__(kFinishThreads, 3) decode_finish(const __grid_constant__ DecodeParams p, int row_blocks) {
   const DecodeArgs& a = p.a;
@@ -869,6 +871,7 @@ __global__ void __launch_bounds__(kFinishThreads, 3) decode_finish(const __grid_
         a.lse[static_cast<long long>(h) * a.B * a.n + tok] =
             st.y == 0.f ? -INFINITY : (st.x + log2f(st.y)) * 0.69314718055994531f;
     }
+    if (!waited) pdl_wait();
     return;
   }
 
@@ -943,6 +946,7 @@ __global__ void __launch_bounds__(kFinishThreads, 3) decode_finish(const __grid_
         __syncthreads();
       }
     }
+    if (!waited) pdl_wait();
   }
 }
 

@@ -2,6 +2,9 @@
 call, workspace sizes follow the problem, and the oracle's rows and eviction rule are
 pinned by hand."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -114,6 +117,46 @@ def test_decode_binding_checks_tensors(L):
         S._pages("cache", cache, 4, 2, 128, torch.bfloat16, dev)
     with pytest.raises(ValueError, match="dtype"):
         S.Decode(**GOOD, dtype="fp16")
+
+
+PROGRAM = r"""
+#include <stdio.h>
+#include "stem.h"
+int main(void) {
+  stem_decode_t d = {0};
+  stem_evict_t e = {0};
+  stem_paged_kv_t none = {0};
+  d.num_seqs = 3; d.q_len = 1; d.num_q_heads = 8; d.num_kv_heads = 2; d.head_dim = 128; d.dtype = STEM_DT_BF16;
+  d.max_kv_len = 1000;
+  e.num_seqs = 3; e.num_kv_heads = 2; e.head_dim = 128; e.dtype = STEM_DT_BF16; e.max_kv_len = 1000; e.budget = 100;
+  if (stem_decode(&d, 0, &none, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) != STEM_ERR_INVALID) return 10;
+  if (stem_evict(&e, &none, 0, 0, 0, &none, 0, 0, 0, 0, 0, 0, 0) != STEM_ERR_INVALID) return 11;
+  if (stem_last_error()[0] == 0) return 12;
+  printf("%zu %zu\n", stem_decode_workspace_size(&d), stem_evict_workspace_size(&e));
+  return 0;
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")
+def test_decoding_entry_points_from_c99(L, tmp_path):
+    """A C99 program links the decoding entry points and gets the sizes the binding gets."""
+    lib_dir = os.path.dirname(S.LIB_PATH)
+    src, exe = tmp_path / "d.c", tmp_path / "d"
+    src.write_text(PROGRAM)
+    cc = subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", str(src), "-I",
+                         os.path.dirname(S.HEADER), "-L", lib_dir, "-lstem", "-Wl,-rpath," + lib_dir, "-o", str(exe)],
+                        capture_output=True, text=True)
+    assert cc.returncode == 0, cc.stderr
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert run.returncode == 0, (run.returncode, run.stdout, run.stderr)
+    assert run.stdout.split() == [str(S.Decode(**GOOD).workspace_bytes()), "256"]
+
+
+def test_library_exports_the_decoding_entry_points(L):
+    names = S.header_functions()
+    for n in ("stem_decode", "stem_decode_workspace_size", "stem_evict", "stem_evict_workspace_size"):
+        assert n in names and hasattr(L, n)
 
 
 def test_oracle_decode_rows_by_hand():

@@ -168,6 +168,21 @@ CASES = {
     "weights_fp8": dict(lens=LENS, Hq=8, Hkv=2, d=128, dtype="fp8_e4m3", weights=True),
     "weights_prefix": dict(lens=[5, 0, 130], Hq=8, Hkv=2, d=128, prefix=200, weights=True),
     "weights_prefix_wide": dict(lens=[5, 0, 130] * 9, Hq=8, Hkv=2, d=128, prefix=400, weights=True),
+    "kv7": dict(lens=[130, 1, 64], Hq=7, Hkv=7, d=128),
+    "kv11_q2": dict(lens=[130, 0, 65], Hq=22, Hkv=11, d=64, q_len=2),
+    "kv5_fp8": dict(lens=[700, 9], Hq=5, Hkv=5, d=128, dtype="fp8_e4m3"),
+    "gqa256_prefix": dict(lens=[3, 65], Hq=256, Hkv=1, d=64, prefix=70),
+    "gqa128_prefix": dict(lens=[3, 65], Hq=128, Hkv=1, d=128, prefix=300),
+    "gqa100_prefix": dict(lens=[3, 65, 0], Hq=100, Hkv=1, d=64, prefix=129),
+    "gqa64_prefix_fp8": dict(lens=[9, 1, 20], Hq=64, Hkv=1, d=128, prefix=257, dtype="fp8_e4m3"),
+    "prefix_wide_1": dict(lens=[1] * 50, Hq=2, Hkv=2, d=128, prefix=1),
+    "prefix_wide_128": dict(lens=[2] * 20, Hq=8, Hkv=2, d=64, prefix=128),
+    "prefix_wide_kv5": dict(lens=[5] * 30, Hq=20, Hkv=5, d=128, prefix=190),
+    "prefix_wide_long": dict(lens=[3, 900] * 10, Hq=12, Hkv=2, d=128, prefix=9001),
+    "prefix_wide_empty_own": dict(lens=[0] * 40, Hq=4, Hkv=2, d=64, prefix=100),
+    "weights_prefix_wide_fp8": dict(lens=[70, 1] * 12, Hq=8, Hkv=2, d=128, prefix=200, q_len=2, dtype="fp8_e4m3", weights=True),
+    "longest": dict(lens=[262144], Hq=1, Hkv=1, d=64),
+    "most_sequences": dict(lens=[1 + b % 3 * 40 for b in range(1024)], Hq=2, Hkv=1, d=64),
     "bound_above_lengths": dict(lens=[5, 100], Hq=4, Hkv=2, d=64, max_kv_len=5000, weights=True),
 }
 
@@ -225,12 +240,12 @@ def test_weights_in_place_and_without_input():
         assert torch.allclose(fresh[b, :, :n] + s.w_in[b, :, :n], apart[b, :, :n], rtol=2.0 ** -23, atol=0)
 
 
-@pytest.mark.parametrize("prefix", [0, 500])
-def test_captured_step_follows_the_lengths(prefix):
+@pytest.mark.parametrize("prefix,more", [(0, 0), (500, 0), (500, 20)])
+def test_captured_step_follows_the_lengths(prefix, more):
     """A captured step replayed as the sequences grow equals the call made anew."""
-    s = Setup([700, 130, 64], Hq=8, Hkv=2, d=128, prefix=prefix, weights=True, seed=8)
+    s = Setup([700, 130, 64] + [5] * more, Hq=8, Hkv=2, d=128, prefix=prefix, weights=True, seed=8)
     ws = S.decode_workspace(s.dec)
-    out = torch.empty((3, 8, 128), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty((3 + more, 8, 128), dtype=torch.bfloat16, device="cuda")
     s.call(out=out, ws=ws)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
@@ -238,7 +253,7 @@ def test_captured_step_follows_the_lengths(prefix):
                       weights_out=s.w_out, out=out, lse=s.lse, ws=ws)
     full = list(s.lens)
     for lens in ([1, 1, 1], [65, 0, 64], [699, 129, 3], full):
-        s.kv_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        s.kv_lens[:3] = torch.tensor(lens[:3], dtype=torch.int32)
         s.w_out.fill_(-5.0)
         g.replay()
         got, got_lse, got_w = out.clone(), s.lse.clone(), s.w_out.clone()
@@ -281,6 +296,80 @@ def test_writes_only_its_buffers(name):
         assert g is None or g.intact()
     for x, y in zip(snap, (s.cache.k_cache.view(torch.uint8), s.cache.v_cache.view(torch.uint8), s.cache.block_table, s.q.view(torch.uint8), s.kv_lens)):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_what_follows_in_the_stream_sees_the_result(prefix):
+    """Calls, copies of their outputs and changes of their inputs in one stream, nothing
+    waited for in between (short sequences: no row is shared by two CTAs)."""
+    s = Setup([9, 64, 1, 30] * 20, Hq=8, Hkv=2, d=128, prefix=prefix, seed=14)
+    ws = S.decode_workspace(s.dec)
+    q0 = s.q.clone()
+    qs = [q0.roll(i, 0).contiguous() for i in range(6)]
+    want = []
+    for q in qs:
+        s.q.copy_(q)
+        want.append(s.call(ws=ws).clone())
+        torch.cuda.synchronize()
+    out, got = torch.empty_like(want[0]), []
+    for _ in range(3):
+        for q in qs:
+            s.q.copy_(q)
+            S.stem_decode(s.dec, s.q, s.cache, s.kv_lens, prefix_table=s.prefix_table, out=out, ws=ws)
+            got.append(out.clone())
+            out.zero_()
+    for i, x in enumerate(got):
+        assert torch.equal(x, want[i % 6]), i
+
+
+def test_pages_beyond_32_bit_offsets():
+    """Pages at the far end of a cache of more than 4 GB (per tensor) give what the same rows
+    give in a small one, through the own and the prefix path, and moved by an eviction."""
+    s = Setup([130, 64] + [7] * 20, Hq=32, Hkv=8, d=128, prefix=100, seed=15)
+    want = s.call().clone()
+    slots = 36000
+    assert slots * PAGE * 8 * 128 * 2 > 1 << 32
+    near = s.cache.k_cache.shape[0]
+    k = torch.empty((slots, PAGE, 8, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    k[slots - near:].copy_(s.cache.k_cache)
+    v[slots - near:].copy_(s.cache.v_cache)
+    far = slots - near
+    cache = S.PagedKV(k, v, s.cache.block_table + far)
+    out = S.stem_decode(s.dec, s.q, cache, s.kv_lens, prefix_table=s.prefix_table + far, lse=s.lse)
+    assert torch.equal(out, want)
+    w = torch.rand((22, 8, 192), device="cuda")
+    ev = S.Evict(22, 8, 128, max_kv_len=130, budget=50, recent=5)
+    fresh = torch.arange(22, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    small = S.PagedKV(torch.zeros((22, PAGE, 8, 128), dtype=torch.bfloat16, device="cuda"),
+                      torch.zeros((22, PAGE, 8, 128), dtype=torch.bfloat16, device="cuda"), fresh)
+    keep, lens = S.stem_evict(ev, s.cache, s.kv_lens, w, small)
+    keep2, lens2 = S.stem_evict(ev, cache, s.kv_lens, w, S.PagedKV(k, v, fresh + (far - 22)))
+    assert torch.equal(keep, keep2) and torch.equal(lens, lens2)
+    for b, n in enumerate(lens.tolist()):
+        assert torch.equal(k[far - 22 + b, :n].view(torch.int16), small.k_cache[b, :n].view(torch.int16))
+        assert torch.equal(v[far - 22 + b, :n].view(torch.int16), small.v_cache[b, :n].view(torch.int16))
+
+
+def test_two_graphs_take_turns_on_one_workspace():
+    """Two captured problems of other shapes that share a workspace, replayed in turn."""
+    a = Setup([3000, 64], Hq=8, Hkv=2, d=128, seed=16)
+    b = Setup([65, 9, 700] * 8, Hq=8, Hkv=2, d=64, prefix=130, weights=True, seed=17)
+    ws = torch.zeros(max(a.dec.workspace_bytes(), b.dec.workspace_bytes()), dtype=torch.uint8, device="cuda")
+    outs, graphs, want = [], [], []
+    for s in (a, b):
+        want.append(s.call(ws=ws).clone())
+        out = torch.empty_like(want[-1])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            S.stem_decode(s.dec, s.q, s.cache, s.kv_lens, prefix_table=s.prefix_table, weights_in=s.w_in, weights_out=s.w_out, out=out, ws=ws)
+        outs.append(out)
+        graphs.append(g)
+    for _ in range(4):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
 
 
 def test_bad_pages_and_lengths_are_reported():

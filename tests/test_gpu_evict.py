@@ -115,6 +115,10 @@ CASES = {
     "one_cache": dict(lens=[700, 130, 64], Hkv=2, d=128, budget=100, sink=4, recent=30, one_cache=True),
     "bound_above_lengths": dict(lens=[300, 20], Hkv=2, d=64, budget=100, max_kv_len=30000),
     "budget_above_bound": dict(lens=[300, 20], Hkv=2, d=64, budget=5000),
+    "longest": dict(lens=[262144, 70], Hkv=1, d=64, budget=30000, sink=4, recent=100),
+    "longest_equal": dict(lens=[262144], Hkv=1, d=64, budget=200000, kind="equal"),
+    "over_128k": dict(lens=[140001], Hkv=2, d=64, budget=1000, sink=4, recent=100, kind="odd"),
+    "most_sequences": dict(lens=[b % 200 for b in range(1024)], Hkv=1, d=64, budget=90, recent=9),
     "many_heads": dict(lens=[200, 90], Hkv=200, d=64, budget=70, recent=8),
 }
 
