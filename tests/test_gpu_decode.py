@@ -193,6 +193,14 @@ def test_decode_matches_oracle(name):
     s.check(s.call())
 
 
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "bf16"), (128, "fp8_e4m3")])
+@pytest.mark.parametrize("prefix", [1, 63, 64, 65, 127, 128, 129, 192, 256, 257, 384, 640, 1500])
+def test_prefix_lengths_around_its_tiles(d, dtype, prefix):
+    """A wide batch over prefixes of a few tiles, with no own token and with a few."""
+    s = Setup([0, 0, 3] * 14, Hq=8, Hkv=2, d=d, prefix=prefix, seed=prefix, dtype=dtype)
+    s.check(s.call())
+
+
 def test_many_sequences():
     """More sequences than a CTA has threads, of every length."""
     rng = np.random.default_rng(3)
