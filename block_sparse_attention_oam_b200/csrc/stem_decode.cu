@@ -27,8 +27,6 @@
 // runs through the rest of its units without computing.
 #include <string.h>
 
-#include <cuda_bf16.h>
-
 #include <type_traits>
 
 #include "stem_internal.cuh"
@@ -679,430 +677,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) decode_kernel(con
   }
 }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
-// ------------------------------------------------- FP8, one new token per sequence: tcgen05
-// Widening codes to f16 keeps the special-function pipe 82 % busy above, so here the codes go
-// to the tensor core as they are.  The roles of rows and tokens are swapped: S^T = K Q^T with
-// 128 tokens (two pages) as M and the unit's up to 16 rows as N, and O^T = V^T P^T with the 128
-// channels as M and the tokens as the sum.  A thread is a token: it reads its rows' scores
-// from TMEM, and the only exponentials are those of real rows (4 per token where the mma.sync
-// form computes 16 x 16 / 32).  P has to be 8 bits too, and e4m3 would lose 2^-4 of every
-// weight, so it goes in as three e4m3 terms, each the rounded remainder of those before:
-// P 2^8 = hi + mid + lo, off by 2^-12 of itself or 2^-10 of 2^8; N = 16 makes a term cheap (16 KB of
-// V through the core, 128 cycles of the 1400 that its bytes take to come).
-// The running maximum belongs to the whole tile (the sum runs over all its tokens), so the
-// four warps vote on every tile whether it grew by more than 2^0.75 (256 * 2^0.75 < 448).
-//   warps 0..3  softmax and epilogue; warp 4 TMA producer; warp 5 MMA issuer.
-// One CTA per SM, a ring of six 32 KB stages.  Drafted tokens (q_len > 1) stay with
-// decode_kernel: a V row that some rows must not see cannot be kept out of a shared product.
-namespace fp8 {
-constexpr int D = 128, kThreads8 = 192, kTok = 128;      // tokens of a tile
-constexpr int NST = 6, PAGE_TILE = 64 * D, TILE = 2 * PAGE_TILE, STAGE = 2 * TILE;
-constexpr int PTERM = 16 * kTok, PBUF = 3 * PTERM, QBUF = 16 * D;
-constexpr int OFF_P = NST * STAGE, OFF_Q = OFF_P + 2 * PBUF, OFF_RED = OFF_Q + 2 * QBUF;
-constexpr int OFF_BAR = OFF_RED + 512;                   // float [2][4][16]
-constexpr int OFF_CUM = OFF_BAR + 512;
-constexpr int SMEM = OFF_CUM + (STEM_MAX_DECODE_SEQS + 1) * 4 + 1024;
-static_assert(SMEM <= 227 * 1024 && SMEM > 114 * 1024, "one CTA per SM");
-constexpr uint32_t kCols = 128;                          // TMEM: four S^T and two O^T of 16 columns
-constexpr uint32_t IDESC_S = instr_desc(0, 0, 0, kTok, 16), IDESC_PV = instr_desc(0, 1, 0, D, 16);
-constexpr float kGrow = 0.75f;
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-  tmem_wait_ld();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
-      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
-      : "memory");
-}
-__device__ __forceinline__ bool vote_any(bool mine) {
-  uint32_t any;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(any)
-      : "r"(mine ? 1u : 0u)
-      : "memory");
-  return any != 0;
-}
-__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// The CTA's tiles one after another, over its units.
-struct Tiles {
-  Walk walk;
-  Seg sg;
-  int pg;     // first page of the next tile
-  int u, g;   // unit and tile numbers of the current tile
-  bool first, last;
-  __device__ __forceinline__ bool next(const DecodeParams& p, const int* cum) {
-    first = false;
-    if (u < 0 || pg >= sg.p1) {
-      if (!walk.next(p, cum, &sg)) return false;
-      pg = sg.p0;
-      ++u;
-      first = true;
-    }
-    ++g;
-    pg += 2;
-    last = pg >= sg.p1;
-    return true;
-  }
-};
-
-template <bool SCORES>
-__global__ void __launch_bounds__(kThreads8, 1) decode_fp8_kernel(const __grid_constant__ DecodeParams p) {
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* smem =
-      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sbase = smem_u32(smem), sP = sbase + OFF_P, sQ = sbase + OFF_Q, b0 = sbase + OFF_BAR;
-  auto full = [&](int s) { return b0 + 8 * s; };
-  auto empty = [&](int s) { return b0 + 48 + 8 * s; };
-  auto s_full = [&](int i) { return b0 + 96 + 8 * i; };
-  auto p_full = [&](int i) { return b0 + 128 + 8 * i; };
-  auto p_empty = [&](int i) { return b0 + 144 + 8 * i; };
-  auto o_full = [&](int i) { return b0 + 160 + 8 * i; };
-  auto o_empty = [&](int i) { return b0 + 176 + 8 * i; };
-  auto q_full = [&](int i) { return b0 + 192 + 8 * i; };
-  const uint32_t bar_drain = b0 + 208;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_BAR + 224);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_BAR + 232);
-  int* warp_sums = reinterpret_cast<int*>(smem + OFF_BAR + 256);
-  int* cum = reinterpret_cast<int*>(smem + OFF_CUM);
-  const DecodeArgs& a = p.a;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const unsigned all = 0xffffffffu;
-  if (tid == 0) {
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
-    }
-    for (int i = 0; i < 4; ++i) mbar_init(s_full(i), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(p_full(i), 4);
-      mbar_init(p_empty(i), 1);
-      mbar_init(o_full(i), 1);
-      mbar_init(o_empty(i), 4);
-      mbar_init(q_full(i), 4);
-    }
-    mbar_init(bar_drain, 1);
-    *abort_flag = 0;
-    mbar_fence_init();
-    tma_prefetch_map(&p.tk);
-    tma_prefetch_map(&p.tv);
-  }
-  if (warp == 5) {
-    tmem_alloc(smem_u32(tmem_slot), kCols);
-    tmem_relinquish();
-  }
-  pdl_wait();     // nothing of the caller's, nor the workspace, is touched before
-  pdl_trigger();  // not earlier: what follows relies on this wait (prefix_kernel, decode_finish)
-  const int run = line_places<kThreads8>(p, cum, warp_sums, [&](int raw) {
-    if (blockIdx.x == 0 && (raw < 0 || raw > a.max_kv_len)) atomicOr(a.status, kStatusBounds);
-  });
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int gang_no = static_cast<int>(blockIdx.x) / p.gang, rank = static_cast<int>(blockIdx.x) % p.gang;
-  const int per = (run + p.gangs - 1) / p.gangs;
-  const int t0 = min(run, gang_no * per), t1 = min(run, t0 + per);
-  const Walk start{t0, t1, 0, rank, -1, 0, 0};
-
-  if (warp == 4) {
-    // ------------------------------------------------------------ producer
-    // 32 pages of a unit at a time, a lane each, looked up one batch ahead
-    Walk walk = start;
-    Seg now_sg, sg;
-    int q0 = 0;
-    bool have = walk.next(p, cum, &sg);
-    auto look = [&]() {
-      const int32_t* table = sg.own ? a.table + static_cast<long long>(sg.b) * a.max_pages : a.prefix_table;
-      return q0 + lane < sg.p1 ? __ldg(table + q0 + lane) : 0;
-    };
-    int ahead = 0;
-    if (have) {
-      q0 = sg.p0;
-      ahead = look();
-    }
-    uint32_t it = 0;
-    bool alive = true;
-    while (have && alive) {
-      now_sg = sg;
-      const int cnt = min(32, sg.p1 - q0);
-      int mine = ahead;
-      q0 += 32;
-      if (q0 >= sg.p1) {
-        have = walk.next(p, cum, &sg);
-        if (have) q0 = sg.p0;
-      }
-      if (have) ahead = look();
-      if (mine < 0 || mine >= a.num_slots) {
-        atomicOr(a.status, kStatusBounds);
-        mine = 0;
-      }
-      for (int q = 0; q < cnt; q += 2, ++it) {
-        const int ra = __shfl_sync(all, mine, q) * kTile, rb = __shfl_sync(all, mine, (q + 1) & 31) * kTile;
-        const int st = it % NST;
-        const bool ok = mbar_wait(empty(st), ((it / NST) & 1) ^ 1, abort_flag, a.status);
-        if (!__all_sync(all, ok)) {
-          alive = false;
-          break;
-        }
-        if (lane == 0) {
-          const uint32_t dst = sbase + st * STAGE;
-          const bool two = q + 1 < cnt;
-          mbar_arrive_expect_tx(full(st), two ? STAGE : STAGE / 2);
-          tma_load_3d(dst, &p.tk, full(st), 0, now_sg.kvh, ra);
-          if (two) tma_load_3d(dst + PAGE_TILE, &p.tk, full(st), 0, now_sg.kvh, rb);
-          tma_load_3d(dst + TILE, &p.tv, full(st), 0, now_sg.kvh, ra);
-          if (two) tma_load_3d(dst + TILE + PAGE_TILE, &p.tv, full(st), 0, now_sg.kvh, rb);
-        }
-      }
-    }
-    if (!alive)  // let the copies already issued land before the CTA can exit
-      for (uint32_t q = it > NST ? it - NST : 0; q < it; ++q)
-        for (int spin = 0; spin < 1000000 && !mbar_try_wait(full(q % NST), (q / NST) & 1); ++spin) {}
-  } else if (warp == 5) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      // S^T runs up to two tiles ahead of P V, over the units' ends; of four S buffers the one
-      // it goes into was read by the softmax before the P of two tiles ago was handed over
-      Tiles ts{start, {}, 0, -1, -1, false, false}, tp = ts;
-      bool s_left = ts.next(p, cum), alive = true;
-      auto issue_s = [&]() -> bool {
-        const int st = ts.g % NST;
-        if (ts.first && !mbar_wait(q_full(ts.u & 1), (ts.u >> 1) & 1, abort_flag, a.status)) return false;
-        if (!mbar_wait(full(st), (ts.g / NST) & 1, abort_flag, a.status)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_fp8(tmem + 16 * (ts.g & 3), smem_desc_sw128(sbase + st * STAGE + k * 32, 16, 1024),
-                  smem_desc_sw128(sQ + (ts.u & 1) * QBUF + k * 32, 16, 1024), IDESC_S, k > 0);
-        mma_commit(s_full(ts.g & 3));
-        s_left = ts.next(p, cum);
-        return true;
-      };
-      while (alive && tp.next(p, cum)) {
-        while (alive && s_left && ts.g <= tp.g + 2) {
-          // not past a unit's start whose Q waits for this unit's tiles to be worked on
-          if (ts.first && ts.g > tp.g && !mbar_try_wait(q_full(ts.u & 1), (ts.u >> 1) & 1)) break;
-          alive = issue_s();
-        }
-        if (!alive) break;
-        const int st = tp.g % NST, pb = tp.g & 1;
-        if (tp.first && !mbar_wait(o_empty(tp.u & 1), ((tp.u >> 1) & 1) ^ 1, abort_flag, a.status)) break;
-        if (!mbar_wait(p_full(pb), (tp.g >> 1) & 1, abort_flag, a.status)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int t = 0; t < 3; ++t)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_fp8(tmem + 64 + 16 * (tp.u & 1), smem_desc_sw128(sbase + st * STAGE + TILE + k * 32 * 128, TILE, 1024),
-                    smem_desc_sw128(sP + pb * PBUF + t * PTERM + k * 32, 16, 1024), IDESC_PV,
-                    !(tp.first && t == 0 && k == 0));
-        mma_commit(empty(st));
-        mma_commit(p_empty(pb));
-        if (tp.last) mma_commit(o_full(tp.u & 1));
-      }
-      // every product of this thread has completed
-      mma_commit(bar_drain);
-      for (int spin = 0; spin < 4000000 && !mbar_try_wait(bar_drain, 0); ++spin) {}
-    }
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------ softmax and epilogue
-    // A wait that runs out leaves the flow as it is (nothing computed is right any more): the
-    // four warps stay together at their barriers.
-    float* red_max = reinterpret_cast<float*>(smem + OFF_RED);      // [4][16]
-    float* red_sum = red_max + 64;
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-    const int G = a.G;
-    auto stage_q = [&](const Seg& s, int u) {  // row tid / 8, piece tid % 8 of 16 bytes
-      const int first = s.rtile * kDecodeRows, r = tid / 8, c = tid % 8;
-      const int nrows = min(kDecodeRows, (s.own ? G : a.B * G) - first);
-      const int row = (s.own ? s.b * G : 0) + first + r, tok = div_g(p, row);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < nrows)
-        v = ld_early(static_cast<const uint4*>(a.q) + (static_cast<long long>(tok) * a.Hq + s.kvh * G + row - tok * G) * 8 + c);
-      *reinterpret_cast<uint4*>(smem + OFF_Q + (u & 1) * QBUF + r * 128 + ((c ^ (r & 7)) << 4)) = v;
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full(u & 1));
-    };
-    Walk walk = start;
-    Seg sg, ahead;
-    bool more = walk.next(p, cum, &ahead);
-    int u = 0, g = 0;
-    if (more) stage_q(ahead, 0);
-    for (; more; ++u) {
-      sg = ahead;
-      // the next unit's Q: its buffer was last read by the unit before this one
-      more = walk.next(p, cum, &ahead);
-      if (more) stage_q(ahead, u + 1);
-      const int first = sg.rtile * kDecodeRows;
-      const int nrows = min(kDecodeRows, (sg.own ? G : a.B * G) - first);
-      const int row_base = (sg.own ? sg.b * G : 0) + first;
-      float* srow = nullptr;
-      if (SCORES && sg.own)
-        srow = a.scores + (static_cast<long long>(sg.b * a.Hkv + sg.kvh) * G + first) * a.score_stride;
-      float m[16], l[16];
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-      }
-      const uint32_t O = tmem + 64 + 16 * (u & 1) + lane_off;
-      for (int pg = sg.p0; pg < sg.p1; pg += 2, ++g) {
-        mbar_wait(s_full(g & 3), (g >> 2) & 1, abort_flag, a.status);
-        __syncwarp();
-        tc_fence_after();
-        float s[16];
-        tmem_ld16(tmem + 16 * (g & 3) + lane_off, s);
-        const int valid = min(sg.len, sg.p1 * kTile) - pg * kTile;  // tokens of this tile
-        const int token = pg * kTile + tid;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = tid < valid ? s[r] * a.scale_log2 : -INFINITY;
-        if (SCORES && sg.own && token < sg.p1 * kTile)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (r < nrows) srow[r * a.score_stride + token] = s[r];
-        bool grow = false;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) grow = grow || (r < nrows && s[r] > m[r] + kGrow);
-        if (vote_any(grow)) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (r < nrows) {
-              float x = s[r];
-#pragma unroll
-              for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(all, x, o));
-              if (lane == 0) red_max[warp * 16 + r] = x;
-            }
-          consumer_sync();
-          float f[16];
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            f[r] = 1.f;
-            if (r < nrows) {
-              const float x = fmaxf(fmaxf(red_max[r], red_max[16 + r]), fmaxf(red_max[32 + r], red_max[48 + r]));
-              const float n = fmaxf(m[r], x);
-              f[r] = n == m[r] ? 1.f : ex2_approx(m[r] - n);
-              m[r] = n;
-              l[r] *= f[r];
-            }
-          }
-          if (pg > sg.p0) {  // what O has so far
-            mbar_wait(p_empty((g - 1) & 1), ((g - 1) >> 1) & 1, abort_flag, a.status);
-            __syncwarp();
-            tc_fence_after();
-            float o[16];
-            tmem_ld16(O, o);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) o[r] *= f[r];
-            tmem_st16(O, o);
-            tmem_wait_st();
-            tc_fence_before();
-          }
-        }
-        // P 2^8 in three e4m3 terms, [row][token] with the 128-byte swizzle
-        mbar_wait(p_empty(g & 1), ((g >> 1) & 1) ^ 1, abort_flag, a.status);
-        __syncwarp();
-        unsigned char* P = smem + OFF_P + (g & 1) * PBUF;
-#pragma unroll
-        for (int r = 0; r < 16; r += 2) {
-          if (r < nrows) {
-            float x = ex2_approx(s[r] - (m[r] == -INFINITY ? 0.f : m[r]) + 8.0f);
-            float y = ex2_approx(s[r + 1] - (m[r + 1] == -INFINITY ? 0.f : m[r + 1]) + 8.0f);
-            if (r + 1 >= nrows) y = 0.f;
-            l[r] += x;
-            l[r + 1] += y;
-            unsigned char* at0 = P + r * 128 + (((tid >> 4) ^ (r & 7)) << 4) + (tid & 15);
-            unsigned char* at1 = P + (r + 1) * 128 + (((tid >> 4) ^ ((r + 1) & 7)) << 4) + (tid & 15);
-#pragma unroll
-            for (int t = 0; t < 3; ++t) {
-              const uint32_t c = pack_e4m3x2(x, y);
-              at0[t * PTERM] = static_cast<unsigned char>(c);
-              at1[t * PTERM] = static_cast<unsigned char>(c >> 8);
-              const float2 back = e4m3x2_to_float2(static_cast<uint16_t>(c));
-              x -= back.x;
-              y -= back.y;
-            }
-          }
-        }
-        if (tid >= valid) {  // V's row may hold anything
-          unsigned char* V = smem + (g % NST) * STAGE + TILE + tid * 128;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(V + 16 * x) = make_uint4(0, 0, 0, 0);
-        }
-        fence_async_shared();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(g & 1));
-      }
-      // epilogue: a thread is a channel now
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (r < nrows) {
-          const float x = warp_sum(l[r]);
-          if (lane == 0) red_sum[warp * 16 + r] = x;
-        }
-      mbar_wait(o_full(u & 1), (u >> 1) & 1, abort_flag, a.status);
-      __syncwarp();
-      tc_fence_after();
-      float o[16];
-      tmem_ld16(O, o);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(o_empty(u & 1));
-      consumer_sync();
-      const bool direct = sg.own && sg.p0 == 0 && sg.p1 == sg.pages && a.prefix_len == 0;
-      const long long slot = static_cast<long long>(gang_no + sg.unit) * p.gang + rank;
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (r < nrows) {
-          const float L = ((red_sum[r] + red_sum[16 + r]) + (red_sum[32 + r] + red_sum[48 + r])) * 0.00390625f;
-          const float v = o[r] * 0.00390625f;
-          if (direct) {
-            const int row = row_base + r, tok = div_g(p, row), h = sg.kvh * G + row - tok * G;
-            const float inv = m[r] == -INFINITY && L == 0.f ? 0.f : a.v_scale / L;
-            static_cast<__nv_bfloat16*>(a.out)[(static_cast<long long>(tok) * a.Hq + h) * D + tid] = __float2bfloat16(v * inv);
-            if (a.lse != nullptr && tid == 0)
-              a.lse[static_cast<long long>(h) * a.B + tok] =
-                  L == 0.f ? -INFINITY : (m[r] + log2f(L)) * 0.69314718055994531f;
-          } else {
-            a.part_o[(slot * a.part_rows + r) * D + tid] = v;
-          }
-          if (tid == 0 && (!direct || SCORES)) a.part_ml[slot * kDecodeRows + r] = make_float2(m[r], L);
-        }
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, kCols);
-}
-}  // namespace fp8
-
 // The partials of one row: number i's (m, l) at ml[i * ml_step], its output at o[i * o_step].
 struct Pieces {
   const float2* ml;
@@ -1148,6 +722,17 @@ __device__ __forceinline__ Pieces prefix_pieces(const DecodeParams& p, int per, 
 // Pages of a sequence from its length on the line.
 __device__ __forceinline__ int pages_on_line(const DecodeParams& p, int length) {
   return length > 0 ? length / (p.head_groups * p.rt) - kDecodeUnitCost : 0;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
 
 // A row's partials, the own ones first.
@@ -1368,16 +953,9 @@ __global__ void __launch_bounds__(kFinishThreads, 3) decode_finish(const __grid_
 template <int D, bool FP8, bool SCORES>
 cudaError_t run(const DecodeParams& prm, cudaStream_t st) {
   using C = Cfg<D, FP8>;
-  cudaError_t e;
-  if (FP8 && prm.a.n == 1) {
-    e = set_smem_once<fp8::decode_fp8_kernel<SCORES>>(fp8::SMEM);
-    if (e == cudaSuccess)
-      e = launch_dependent(fp8::decode_fp8_kernel<SCORES>, prm.gangs * prm.gang, fp8::kThreads8, fp8::SMEM, 1, st, prm);
-  } else {
-    e = set_smem_once<decode_kernel<D, FP8, SCORES>>(C::SMEM);
-    if (e == cudaSuccess)
-      e = launch_dependent(decode_kernel<D, FP8, SCORES>, prm.gangs * prm.gang, kThreads, C::SMEM, 1, st, prm);
-  }
+  cudaError_t e = set_smem_once<decode_kernel<D, FP8, SCORES>>(C::SMEM);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(decode_kernel<D, FP8, SCORES>, prm.gangs * prm.gang, kThreads, C::SMEM, 1, st, prm);
   if (e != cudaSuccess) return e;
   // behind it, so that its partials, the larger ones, are the last into L2
   if (prm.pre.gangs > 0 && (e = launch_prefix(prm.a, prm.pre, FP8, st)) != cudaSuccess) return e;
@@ -1418,9 +996,7 @@ cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st) {
   prm.prt = a.prefix_len > 0 && prm.pre.gangs == 0 ? (a.B * R + kDecodeRows - 1) / kDecodeRows : 0;
   prm.prefix_pages = (a.prefix_len + kTile - 1) / kTile;
   prm.g_magic = a.G > 1 ? static_cast<uint32_t>(((1ull << 32) + a.G - 1) / a.G) : 0u;
-  // decode_fp8_kernel has one CTA per SM: gangs of at most four, which divide 148
-  const bool codes = fp8 && a.n == 1;
-  prm.gang = gang_of(a.Hkv, codes ? 4 : 8);
+  prm.gang = gang_of(a.Hkv);
   prm.head_groups = a.Hkv / prm.gang;
   prm.prefix_span = prm.prt > 0 ? prm.head_groups * prm.prt * (prm.prefix_pages + kDecodeUnitCost) : 0;
   int dev = 0, sms = 0;
@@ -1430,7 +1006,7 @@ cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st) {
   const long long bound = static_cast<long long>(prm.head_groups) *
                           (prm.prt * prm.prefix_pages +
                            static_cast<long long>(a.B) * prm.rt * ((a.max_kv_len + kTile - 1) / kTile));
-  const int resident = (codes ? 1 : (fp8 || a.d == 64 ? 3 : 2)) * (sms < kDecodeSms ? sms : kDecodeSms);  // Cfg::CTAS per SM
+  const int resident = (fp8 || a.d == 64 ? 3 : 2) * (sms < kDecodeSms ? sms : kDecodeSms);  // Cfg::CTAS per SM
   prm.gangs = resident / prm.gang;
   if (bound < prm.gangs) prm.gangs = static_cast<int>(bound);
   const bool scores = a.scores != nullptr;

@@ -581,7 +581,7 @@ PrefixPlan plan_prefix(int B, int n, int Hkv, int G, int prefix_len) {
   const int tokens = B * n;
   // Below two row tiles of decode_kernel its products are as quick and need no second launch.
   if (prefix_len < 1 || G > kRows || static_cast<long long>(tokens) * G <= kPrefixMinRows) return p;
-  p.gang = gang_of(Hkv, 8);
+  p.gang = gang_of(Hkv);
   p.head_groups = Hkv / p.gang;
   p.slot_tokens = kRows / G;
   p.pairs = (tokens + 2 * p.slot_tokens - 1) / (2 * p.slot_tokens);

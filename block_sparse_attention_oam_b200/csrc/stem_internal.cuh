@@ -479,9 +479,9 @@ constexpr int kDecodeUnitCost = 4;
 
 // The kv-heads that CTAs walk side by side: neighbours in memory (a page of one head is 64
 // pieces of 128 or 256 bytes), so that they read whole DRAM rows between them.
-inline int gang_of(int Hkv, int most) {
+inline int gang_of(int Hkv) {
   int gang = 1;
-  for (int g = 2; g <= most; ++g)
+  for (int g = 2; g <= 8; ++g)
     if (Hkv % g == 0) gang = g;
   return gang;
 }
