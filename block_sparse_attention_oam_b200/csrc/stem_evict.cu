@@ -51,15 +51,14 @@ struct EvictParams {
 constexpr uint32_t kNone = 0u;              // behind the last token
 constexpr uint32_t kForced = 0xFFFFFFFFu;   // kept whatever its weight
 __device__ __forceinline__ uint32_t order_key(float w) {
-  if (!(w == w)) w = -INFINITY;
-  const uint32_t u = w == 0.f ? 0u : __float_as_uint(w);
-  return (u >> 31) ? ~u : (u | 0x80000000u);
+  const uint32_t u = __float_as_uint(fmaxf(w + 0.f, -INFINITY));  // -0 + 0 = 0; the maximum of NaN and x is x
+  return u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
 }
 
 // The weight of a key; NaN where several weights have it (zeros of both signs, -inf and NaN)
 // or it stands for none: those are read again.
 __device__ __forceinline__ float key_weight(uint32_t k) {
-  const uint32_t bits = (k >> 31) ? k ^ 0x80000000u : ~k;
+  const uint32_t bits = k ^ (~static_cast<uint32_t>(static_cast<int>(k) >> 31) | 0x80000000u);
   return k == kForced || k == 0x80000000u || k == 0x007FFFFFu ? NAN : __uint_as_float(bits);
 }
 
@@ -78,6 +77,7 @@ struct SelectSmem {
   int coarse[3][kCoarse];          // sums of 32 bins
   int total[kCoarse];              // the same over the cluster, from the top down
   int fine[kMaxCluster][kFine];    // the bins of one group, by CTA, from the top down
+  int group, digit, left;          // of the pass, found by warp 0
   int more[kWarps], same[kWarps];  // keys above the cut-off (forced ones too) and equal to it, by warp
   int counts[2];                   // of the CTA
 };
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
   const int unit = blockIdx.x / C, b = unit / a.Hkv, h = unit % a.Hkv;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const unsigned all = 0xffffffffu;
-  for (int i = tid; i < 2 * kBins; i += kThreads) sm.hist[0][i] = 0;
+  for (int i = tid; i < kBins / 2; i += kThreads) reinterpret_cast<int4*>(sm.hist[0])[i] = make_int4(0, 0, 0, 0);
   pdl_wait();
 
   const int raw = __ldg(a.kv_lens + b);
@@ -131,16 +131,24 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
   const int first = rank * (kThreads * kpt) + warp * (32 * kpt) + lane;           // position of key 0
   uint32_t* key = keys + warp * (32 * kpt) + lane;                                // key e at [32 * e]
   for (int e0 = 0; e0 < kpt; e0 += kBatch) {
+    const int at = first - lane + 32 * e0;  // of the warp's batch
     float v[kBatch];
+    if (at >= lo && at + 32 * kBatch <= hi) {  // all of it to be ranked
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      const int i = first + 32 * (e0 + e);
-      v[e] = i >= lo && i < hi ? w[i] : 0.f;
-    }
+      for (int e = 0; e < kBatch; ++e) v[e] = w[first + 32 * (e0 + e)];
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      const int i = first + 32 * (e0 + e);
-      key[32 * (e0 + e)] = i >= n ? kNone : (i < lo || i >= hi ? kForced : order_key(v[e]));
+      for (int e = 0; e < kBatch; ++e) key[32 * (e0 + e)] = order_key(v[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const int i = first + 32 * (e0 + e);
+        v[e] = i >= lo && i < hi ? w[i] : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const int i = first + 32 * (e0 + e);
+        key[32 * (e0 + e)] = i >= n ? kNone : (i < lo || i >= hi ? kForced : order_key(v[e]));
+      }
     }
   }
   // Runs f(key) over the thread's keys, a batch read ahead: the compiler may not move a
@@ -167,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
       int* hist = sm.hist[pass & 1];
       each([&](uint32_t k) {
-        if (pass == 0 ? k != kNone && k != kForced : k >> (shift + bits) == prefix) atomicAdd(hist + ((k >> shift) & ((1u << bits) - 1)), 1);
+        if (pass == 0 ? k + 1u > 1u : k >> (shift + bits) == prefix) atomicAdd(hist + ((k >> shift) & ((1u << bits) - 1)), 1);
       });
       __syncthreads();
       // Reading all of the other CTAs' bins costs more than the rest (64 KB through distributed
@@ -179,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
       if (tid % 4 == 0) sm.coarse[pass][tid / 4] = sum;
       cluster.sync();
       if (pass == 1)  // every CTA has done with pass 0's bins
-        for (int i = tid; i < kBins; i += kThreads) sm.hist[0][i] = 0;
+        for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<int4*>(sm.hist[0])[i] = make_int4(0, 0, 0, 0);
       int got = 0;
 #pragma unroll
       for (int r = tid % 4; r < kMaxCluster; r += 4)
@@ -188,17 +196,33 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
       got += __shfl_xor_sync(all, got, 2);
       if (tid % 4 == 0) sm.total[tid / 4] = got;
       __syncthreads();
-      // every warp the same: lane l holds groups 2 l and 2 l + 1
-      const int c0 = sm.total[2 * lane], c1 = sm.total[2 * lane + 1];
-      const int pair = find_lane(c0 + c1, &left);
-      const int upper = __shfl_sync(all, c0, pair);
-      const int group = kCoarse - 1 - 2 * pair - (left > upper ? 1 : 0);
-      if (left > upper) left -= upper;
+      if (warp == 0) {  // lane l holds groups 2 l and 2 l + 1
+        const int c0 = sm.total[2 * lane], c1 = sm.total[2 * lane + 1];
+        const int pair = find_lane(c0 + c1, &left);
+        const int upper = __shfl_sync(all, c0, pair);
+        if (lane == 0) {
+          sm.group = kCoarse - 1 - 2 * pair - (left > upper ? 1 : 0);
+          sm.left = left > upper ? left - upper : left;
+        }
+      }
+      __syncthreads();
+      const int group = sm.group;
       if (warp < C) sm.fine[warp][lane] = cluster.map_shared_rank(hist, warp)[kFine * group + kFine - 1 - lane];
       __syncthreads();
-      int f = 0;
-      for (int r = 0; r < C; ++r) f += sm.fine[r][lane];
-      const int digit = kFine * group + kFine - 1 - find_lane(f, &left);
+      if (warp == 0) {
+        int f = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) f += r < C ? sm.fine[r][lane] : 0;
+        left = sm.left;
+        const int digit = kFine * group + kFine - 1 - find_lane(f, &left);
+        if (lane == 0) {
+          sm.digit = digit;
+          sm.left = left;
+        }
+      }
+      __syncthreads();
+      const int digit = sm.digit;
+      left = sm.left;
       prefix = (prefix << bits) | static_cast<uint32_t>(digit);
     }
     cut = prefix;
