@@ -74,7 +74,7 @@ struct DecodeParams {
   int prefix_pages, prefix_span;  // pages of the prefix, its length on the line
   int gang;                  // CTAs that walk together, each with another kv-head of the same pages
   int gangs, head_groups;    // ctas / gang, Hkv / gang
-  PrefixPlan pre;            // gangs > 0: the prefix is prefix_kernel's, behind this one; prt is 0 then
+  PrefixPlan pre;            // gangs > 0: the prefix is prefix_kernel's, ahead of this one; prt is 0 then
   uint32_t g_magic;          // ceil(2^32 / G): x / G = umulhi(x, g_magic) for G > 1 (see div_g)
 };
 
@@ -276,8 +276,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) decode_kernel(con
     tma_prefetch_map(&p.tk);
     tma_prefetch_map(&p.tv);
   }
-  pdl_wait();     // nothing of the caller's, nor the workspace, is touched before
-  pdl_trigger();  // not earlier: what follows relies on this wait (prefix_kernel, decode_finish)
+  // Nothing of the caller's, nor the workspace, is touched before the step's first kernel has
+  // waited: this one, or prefix_kernel, whose CTAs let this launch go after their wait.
+  const bool second = p.pre.gangs > 0;
+  if (!second) pdl_wait();
+  pdl_trigger();  // not earlier: decode_finish relies on that wait
   int* cum = reinterpret_cast<int*>(smem + C::OFF_CUM);
   const int run = line_places<kThreads>(p, cum, warp_sums, [&](int raw) {
     if (blockIdx.x == 0 && (raw < 0 || raw > a.max_kv_len)) atomicOr(a.status, kStatusBounds);
@@ -675,6 +678,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) decode_kernel(con
     }
     if (have) store_q();
   }
+  // decode_finish takes this launch's end for prefix_kernel's too: one CTA that stays for it is
+  // enough, and the others leave their places to the CTAs still to come
+  if (second && blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 // The partials of one row: number i's (m, l) at ml[i * ml_step], its output at o[i * o_step].
@@ -955,10 +961,10 @@ cudaError_t run(const DecodeParams& prm, cudaStream_t st) {
   using C = Cfg<D, FP8>;
   cudaError_t e = set_smem_once<decode_kernel<D, FP8, SCORES>>(C::SMEM);
   if (e != cudaSuccess) return e;
+  if (prm.pre.gangs > 0 && (e = launch_prefix(prm.a, prm.pre, FP8, st)) != cudaSuccess) return e;
   e = launch_dependent(decode_kernel<D, FP8, SCORES>, prm.gangs * prm.gang, kThreads, C::SMEM, 1, st, prm);
   if (e != cudaSuccess) return e;
   // behind it, so that its partials, the larger ones, are the last into L2
-  if (prm.pre.gangs > 0 && (e = launch_prefix(prm.a, prm.pre, FP8, st)) != cudaSuccess) return e;
   const DecodeArgs& a = prm.a;
   const long long rows = static_cast<long long>(a.B) * a.n * a.Hq;
   const long long chunks =
@@ -1006,8 +1012,17 @@ cudaError_t launch_decode(const DecodeArgs& a, bool fp8, cudaStream_t st) {
   const long long bound = static_cast<long long>(prm.head_groups) *
                           (prm.prt * prm.prefix_pages +
                            static_cast<long long>(a.B) * prm.rt * ((a.max_kv_len + kTile - 1) / kTile));
-  const int resident = (fp8 || a.d == 64 ? 3 : 2) * (sms < kDecodeSms ? sms : kDecodeSms);  // Cfg::CTAS per SM
-  prm.gangs = resident / prm.gang;
+  sms = sms < kDecodeSms ? sms : kDecodeSms;
+  const int per_sm = fp8 || a.d == 64 ? 3 : 2;  // Cfg::CTAS
+  prm.gangs = sms * per_sm / prm.gang;
+  // Behind prefix_kernel's launch the CTAs of one round on the SMs that it leaves free, where
+  // that round is likely the shorter of the two (a 64-token tile here takes a quarter of a
+  // 128-key tile there, at which the host's bound on the lengths is compared); otherwise as many
+  // as without a prefix, the later ones starting as places become free.  64 sequences behind
+  // 32768 shared tokens, one round / all: 72 / 72 us at 512 own tokens, 88 / 94 at 1024,
+  // 140 / 125 at 2048, 242 / 196 at 4096.
+  const int beside = (sms - prm.pre.gangs * prm.pre.gang) * per_sm / prm.gang;
+  if (prm.pre.gangs > 0 && beside > 0 && bound <= 4ll * beside * prm.pre.per) prm.gangs = beside;
   if (bound < prm.gangs) prm.gangs = static_cast<int>(bound);
   const bool scores = a.scores != nullptr;
   if (fp8) return scores ? run<128, true, true>(prm, st) : run<128, true, false>(prm, st);

@@ -489,7 +489,11 @@ inline int gang_of(int Hkv) {
 // The shared prefix's split when it runs on the tensor cores (stem_decode_prefix.cu): units
 // of (kv-head, pair of row tiles), each `tiles` 128-key tiles and kPrefixUnitCost empty ones
 // long on a gang member's line, of which every CTA takes `per`.
-constexpr int kPrefixCtas = 148;
+// An SM each, first in the step's stream; decode_kernel runs beside them on the others, for
+// whose loads these products leave the memory free.  64 sequences with 512 tokens behind 32768
+// shared ones: 82 us one kernel after the other on all 148 SMs, 72 with 96 CTAs here (68 with
+// 104, which 256 sequences of 64 tokens behind 8192 shared ones pay: 73 and 79).
+constexpr int kPrefixCtas = 96;
 constexpr int kPrefixTile = 128;
 constexpr int kPrefixUnitCost = 2;
 constexpr int kPrefixMinRows = 32;

@@ -201,6 +201,16 @@ def test_prefix_lengths_around_its_tiles(d, dtype, prefix):
     s.check(s.call())
 
 
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "bf16"), (128, "fp8_e4m3")])
+@pytest.mark.parametrize("prefix,cap", [(70, 1500), (1500, 1500), (70, 60000), (9001, 1500)])
+def test_own_tokens_beside_the_prefix(d, dtype, prefix, cap):
+    """Own tokens that outlast a wide batch's prefix, and a bound far above their number: both
+    kernels at once, and more CTAs than find a place beside the prefix's."""
+    s = Setup([0, 1500, 3, 64, 129] * 5, Hq=8, Hkv=2, d=d, prefix=prefix, seed=prefix + cap, dtype=dtype, max_kv_len=cap,
+              weights=True)
+    s.check(s.call())
+
+
 def test_many_sequences():
     """More sequences than a CTA has threads, of every length."""
     rng = np.random.default_rng(3)
