@@ -130,25 +130,34 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
   const int kpt = kBatch * ((n + C * kThreads * kBatch - 1) / (C * kThreads * kBatch));  // p.kpt at most
   const int first = rank * (kThreads * kpt) + warp * (32 * kpt) + lane;           // position of key 0
   uint32_t* key = keys + warp * (32 * kpt) + lane;                                // key e at [32 * e]
+  __syncthreads();  // the bins are zero
+  // Into shared memory, the next batch on its way, and with them the first digit's counts.
+  float v[kBatch];
+  auto load = [&](int e0) {
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int i = first + 32 * (e0 + e);
+      v[e] = i >= lo && i < hi ? w[i] : 0.f;
+    }
+  };
+  load(0);
   for (int e0 = 0; e0 < kpt; e0 += kBatch) {
     const int at = first - lane + 32 * e0;  // of the warp's batch
-    float v[kBatch];
-    if (at >= lo && at + 32 * kBatch <= hi) {  // all of it to be ranked
+    uint32_t k[kBatch];
 #pragma unroll
-      for (int e = 0; e < kBatch; ++e) v[e] = w[first + 32 * (e0 + e)];
-#pragma unroll
-      for (int e = 0; e < kBatch; ++e) key[32 * (e0 + e)] = order_key(v[e]);
-    } else {
+    for (int e = 0; e < kBatch; ++e) k[e] = order_key(v[e]);
+    if (e0 + kBatch < kpt) load(e0 + kBatch);
+    if (at < lo || at + 32 * kBatch > hi) {  // not all of it to be ranked
 #pragma unroll
       for (int e = 0; e < kBatch; ++e) {
         const int i = first + 32 * (e0 + e);
-        v[e] = i >= lo && i < hi ? w[i] : 0.f;
+        k[e] = i >= n ? kNone : (i < lo || i >= hi ? kForced : k[e]);
       }
+    }
 #pragma unroll
-      for (int e = 0; e < kBatch; ++e) {
-        const int i = first + 32 * (e0 + e);
-        key[32 * (e0 + e)] = i >= n ? kNone : (i < lo || i >= hi ? kForced : order_key(v[e]));
-      }
+    for (int e = 0; e < kBatch; ++e) {
+      key[32 * (e0 + e)] = k[e];
+      if (k[e] + 1u > 1u) atomicAdd(sm.hist[0] + (k[e] >> 21), 1);  // neither kNone nor kForced
     }
   }
   // Runs f(key) over the thread's keys, a batch read ahead: the compiler may not move a
@@ -162,7 +171,6 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
       for (int e = 0; e < kBatch; ++e) f(k[e]);
     }
   };
-  __syncthreads();
 
   // the cut-off key, digit by digit
   uint32_t cut = kForced - 1;  // no weight's key is this large
@@ -174,9 +182,10 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
       int* hist = sm.hist[pass & 1];
-      each([&](uint32_t k) {
-        if (pass == 0 ? k + 1u > 1u : k >> (shift + bits) == prefix) atomicAdd(hist + ((k >> shift) & ((1u << bits) - 1)), 1);
-      });
+      if (pass > 0)
+        each([&](uint32_t k) {
+          if (k >> (shift + bits) == prefix) atomicAdd(hist + ((k >> shift) & ((1u << bits) - 1)), 1);
+        });
       __syncthreads();
       // Reading all of the other CTAs' bins costs more than the rest (64 KB through distributed
       // shared memory for each CTA: 10 us); so first the groups' sums, then the bins of one group.
