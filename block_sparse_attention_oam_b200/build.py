@@ -1,4 +1,5 @@
-"""Build libstem.so (the C-ABI library) in-tree with nvcc for sm_100a."""
+"""Build libstem.so (the C-ABI library) in-tree with nvcc for sm_100a, and stem_binding.so
+(the Python entries of the operators called once per layer and token) with g++."""
 from __future__ import annotations
 
 import glob
@@ -10,6 +11,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libstem.so")
+BINDING = os.path.join(PKG, "stem_binding.so")
+BINDING_SRC = os.path.join(CSRC, "stem_binding.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -34,7 +37,31 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def build_binding(force: bool = False) -> str:
+    deps = [BINDING_SRC, os.path.join(ROOT, "include", "stem.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+        return BINDING
+    import sysconfig
+
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    dirs = [os.path.join(home, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
+            os.path.join(ROOT, "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{d}" for d in dirs), BINDING_SRC,
+           "-o", BINDING + ".tmp", "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}")
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force)
     if not force and not _stale():
         return LIB
     objs = []

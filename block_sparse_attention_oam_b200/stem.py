@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libstem (include/stem.h).
+"""Thin binding of libstem (include/stem.h): ctypes, and for the operators that run once per
+layer and token (stem_decode, stem_evict) a native module, csrc/stem_binding.cpp.
 
 Argument marshalling only: torch tensors provide device memory and the current
 CUDA stream; every step of the path runs in libstem's CUDA kernels.  There is no
@@ -8,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import importlib.util
 import os
 import re
 from typing import Optional, Sequence
@@ -427,20 +429,22 @@ def _pages(name: str, c: PagedKV, num_seqs: int, Hkv: int, d: int, dtype, device
                   _tensor(f"{name}.block_table", table, (num_seqs, width), torch.int32, device), PAGE_SIZE, width, slots)
 
 
-def _raw(stream, device) -> int:
-    """The stream's handle, or that of the device's current stream."""
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+_native = None
 
 
-def _call_on(device, fn, *args) -> None:
-    """Call the library with the tensors' device current."""
-    if device.index == torch.cuda.current_device():
-        status = fn(*args)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args)
-    if status != STEM_OK:
-        _check(status)
+def _binding():
+    """The native module and libstem's entry points for it.  Raises if it is missing."""
+    global _native
+    if _native is None:
+        path = os.path.join(_PKG, "stem_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m block_sparse_attention_oam_b200.build`")
+        spec = importlib.util.spec_from_file_location("stem_binding", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        entry = [ctypes.cast(getattr(lib(), f), _P).value for f in ("stem_decode", "stem_evict")]
+        _native = (m.decode, entry[0], m.evict, entry[1])
+    return _native
 
 
 def decode_workspace(dec: Decode, device="cuda") -> torch.Tensor:
@@ -463,22 +467,27 @@ def stem_decode(dec: Decode, q, cache: PagedKV, kv_lens, prefix_table=None, weig
         ws = decode_workspace(dec, dev)
     if dec.weights != (weights_out is not None) or (weights_in is not None and weights_out is None):
         raise ValueError("weights_out goes with Decode(weights=True), weights_in with weights_out")
-    i32, f32, stride, prefix = torch.int32, torch.float32, 0, None
-    if prefix_table is not None:
-        prefix = _tensor("prefix_table", prefix_table, (-(-dec.prefix_len // PAGE_SIZE),), i32, dev)
-    w_in = w_out = None
-    if weights_out is not None:
-        stride = weights_out.shape[-1]
-        w_out = _tensor("weights_out", weights_out, (B, Hkv, stride), f32, dev)
+    call, entry, _, _ = _native or _binding()
+    status = call(entry, dec._c, q, cache.k_cache, cache.v_cache, cache.block_table, kv_lens, prefix_table, weights_in,
+                  weights_out, out, lse, ws, None if stream is None else stream.cuda_stream)
+    if status < 0:  # which tensor it is
+        i32, f32, T = torch.int32, torch.float32, B * n
+        _tensor("q", q, (T, Hq, d), dec._torch, dev)
+        _pages("cache", cache, B, Hkv, d, dec._torch, dev)
+        _tensor("kv_lens", kv_lens, (B,), i32, dev)
+        if prefix_table is not None:
+            _tensor("prefix_table", prefix_table, (-(-dec.prefix_len // PAGE_SIZE),), i32, dev)
+        if weights_out is not None:
+            _tensor("weights_out", weights_out, (B, Hkv, None), f32, dev)
         if weights_in is not None:
-            w_in = _tensor("weights_in", weights_in, (B, Hkv, stride), f32, dev)
-    T = B * n
-    size = ws.numel()
-    _call_on(dev, lib().stem_decode, dec.c, _tensor("q", q, (T, Hq, d), dec._torch, dev),
-             _pages("cache", cache, B, Hkv, d, dec._torch, dev), _tensor("kv_lens", kv_lens, (B,), i32, dev), prefix,
-             w_in, w_out, stride, _tensor("out", out, (T, Hq, d), torch.bfloat16, dev),
-             None if lse is None else _tensor("lse", lse, (Hq, T), f32, dev),
-             _tensor("ws", ws, (size,), torch.uint8, dev), size, _raw(stream, dev))
+            _tensor("weights_in", weights_in, (B, Hkv, weights_out.shape[-1]), f32, dev)
+        _tensor("out", out, (T, Hq, d), torch.bfloat16, dev)
+        if lse is not None:
+            _tensor("lse", lse, (Hq, T), f32, dev)
+        _tensor("ws", ws, (None,), torch.uint8, dev)
+        raise ValueError("an argument does not fit the problem")
+    if status != STEM_OK:
+        _check(status)
     return out
 
 
@@ -522,7 +531,7 @@ def stem_evict(ev: Evict, src: PagedKV, kv_lens, weights, dst: PagedKV, kv_lens_
     their K/V rows go in order to dst's pages, which must be others than those read.
     Returns (keep, kv_lens_out): kept positions [num_seqs, Hkv, budget], -1 behind the last,
     and the new lengths; weights_out [num_seqs, Hkv, stride >= budget] is written if given."""
-    B, Hkv, d, dev, f32 = ev.num_seqs, ev.num_kv_heads, ev.head_dim, weights.device, torch.float32
+    B, Hkv, d, dev = ev.num_seqs, ev.num_kv_heads, ev.head_dim, weights.device
     if dev.type != "cuda":
         raise ValueError("stem_evict takes CUDA tensors")
     if kv_lens_out is None:
@@ -531,16 +540,24 @@ def stem_evict(ev: Evict, src: PagedKV, kv_lens, weights, dst: PagedKV, kv_lens_
         keep = torch.empty((B, Hkv, ev.budget), dtype=torch.int32, device=dev)
     if ws is None:
         ws = evict_workspace(ev, dev)
-    i32, stride, size = torch.int32, weights.shape[-1], ws.numel()
-    w_out, out_stride = None, 0
-    if weights_out is not None:
-        out_stride = weights_out.shape[-1]
-        w_out = _tensor("weights_out", weights_out, (B, Hkv, out_stride), f32, dev)
-    _call_on(dev, lib().stem_evict, ev.c, _pages("src", src, B, Hkv, d, ev._torch, dev),
-             _tensor("kv_lens", kv_lens, (B,), i32, dev), _tensor("weights", weights, (B, Hkv, stride), f32, dev), stride,
-             _pages("dst", dst, B, Hkv, d, ev._torch, dev), _tensor("kv_lens_out", kv_lens_out, (B,), i32, dev), w_out,
-             out_stride, _tensor("keep", keep, (B, Hkv, ev.budget), i32, dev),
-             _tensor("ws", ws, (size,), torch.uint8, dev), size, _raw(stream, dev))
+    _, _, call, entry = _native or _binding()
+    status = call(entry, ev._c, weights, src.k_cache, src.v_cache, src.block_table, dst.k_cache, dst.v_cache,
+                  dst.block_table, kv_lens, kv_lens_out, weights_out, keep, ws,
+                  None if stream is None else stream.cuda_stream)
+    if status < 0:  # which tensor it is
+        i32, f32 = torch.int32, torch.float32
+        _tensor("weights", weights, (B, Hkv, None), f32, dev)
+        _pages("src", src, B, Hkv, d, ev._torch, dev)
+        _pages("dst", dst, B, Hkv, d, ev._torch, dev)
+        _tensor("kv_lens", kv_lens, (B,), i32, dev)
+        _tensor("kv_lens_out", kv_lens_out, (B,), i32, dev)
+        if weights_out is not None:
+            _tensor("weights_out", weights_out, (B, Hkv, None), f32, dev)
+        _tensor("keep", keep, (B, Hkv, ev.budget), i32, dev)
+        _tensor("ws", ws, (None,), torch.uint8, dev)
+        raise ValueError("an argument does not fit the problem")
+    if status != STEM_OK:
+        _check(status)
     return keep, kv_lens_out
 
 

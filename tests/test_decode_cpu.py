@@ -119,6 +119,32 @@ def test_decode_binding_checks_tensors(L):
         S.Decode(**GOOD, dtype="fp16")
 
 
+def test_native_entries_refuse_without_a_call(L):
+    """Host tensors, other things than tensors, a wrong problem or a wrong number of arguments
+    never reach the library (whose entry point is given as an address that holds no code)."""
+    decode, _, evict, _ = S._binding()
+    dec, ev = S.Decode(**GOOD), S.Evict(3, 2, 128, 1024, 64)
+    q = torch.zeros((3, 8, 128), dtype=torch.bfloat16)
+    k, table, lens = torch.zeros((4, 64, 2, 128), dtype=torch.bfloat16), torch.zeros((3, 16), dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    rest = (k, k, table, lens, None, None, None, q, None, torch.zeros(8, dtype=torch.uint8), None)
+    assert decode(8, dec._c, q, *rest) == -1
+    assert decode(8, dec._c, None, *rest) == -1
+    w, ws = torch.zeros(3, 2, 1024), torch.zeros(8, dtype=torch.uint8)
+    rest_e = (k, k, table, k, k, table, lens, lens, None, torch.zeros((3, 2, 64), dtype=torch.int32), ws, None)
+    assert evict(8, ev._c, w, *rest_e) == -1
+    assert evict(8, ev._c, w[0], *rest_e) == -1
+    with pytest.raises(ValueError):
+        decode(0, dec._c, q, *rest)
+    with pytest.raises(ValueError):
+        decode(8, ev._c, q, *rest)
+    with pytest.raises(TypeError):
+        decode(8, dec, q, *rest)
+    with pytest.raises(TypeError):
+        decode(8, dec._c, q)
+    with pytest.raises(TypeError):
+        evict(8, ev._c)
+
+
 PROGRAM = r"""
 #include <stdio.h>
 #include "stem.h"

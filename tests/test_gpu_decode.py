@@ -390,6 +390,38 @@ def test_two_graphs_take_turns_on_one_workspace():
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
 
 
+@pytest.mark.parametrize("name", ["q", "cache.k_cache", "cache.v_cache", "cache.block_table", "kv_lens", "prefix_table",
+                                  "weights_in", "weights_out", "out", "lse", "ws"])
+def test_tensors_that_do_not_fit_are_named(name):
+    """Another type, another shape, strides, and host memory: refused before anything runs."""
+    s = Setup([5, 70], Hq=8, Hkv=2, d=128, prefix=100, weights=True)
+    out = torch.full_like(s.q, 7.0)
+    ws = S.decode_workspace(s.dec)
+    args = {"q": s.q, "cache.k_cache": s.cache.k_cache, "cache.v_cache": s.cache.v_cache, "cache.block_table": s.cache.block_table,
+            "kv_lens": s.kv_lens, "prefix_table": s.prefix_table, "weights_in": s.w_in, "weights_out": s.w_out, "out": out,
+            "lse": s.lse, "ws": ws}
+
+    def call(**kw):
+        x = args | kw
+        return S.stem_decode(s.dec, x["q"], S.PagedKV(x["cache.k_cache"], x["cache.v_cache"], x["cache.block_table"]),
+                             x["kv_lens"], prefix_table=x["prefix_table"], weights_in=x["weights_in"],
+                             weights_out=x["weights_out"], out=x["out"], lse=x["lse"], ws=x["ws"])
+
+    t = args[name]
+    wide = torch.zeros((*t.shape, 2), dtype=t.dtype, device=t.device)
+    with pytest.raises((ValueError, S.StemError)):  # no width: some of these the library itself refuses
+        call(**{name: t[..., :0]})
+    for x in (t.cpu(), t.to(torch.float64), wide[..., 0], wide):
+        if name == "q" and not x.is_cuda:
+            with pytest.raises(ValueError):
+                call(**{name: x})
+        else:
+            with pytest.raises(ValueError, match=name.replace(".", "[.]") if name != "cache.k_cache" else "cache[.]"):
+                call(**{name: x})
+    torch.cuda.synchronize()
+    assert (out == 7).all()
+
+
 def test_bad_pages_and_lengths_are_reported():
     """A page outside the cache is read as slot 0, a length outside [0, max_kv_len] is
     clamped; both are reported, and the sequences beside them are right."""
