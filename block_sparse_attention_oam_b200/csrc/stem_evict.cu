@@ -13,6 +13,11 @@
 //                 (budget rows read and written, K and V), so each thread keeps eight
 //                 16-byte loads in flight; heads are the inner index, as they are in
 //                 memory, so that rows kept by several heads are read side by side.
+// Measured on one B200: four BF16 caches of 32K tokens and 8 heads of 128 to 8K each, 62 us
+// (selection 15, move 47 of 42 at the copy rate); 32 ragged FP8 caches of up to 64K, 247 us
+// (72 and 176 of 164).  The selection is barriers, waits on other CTAs and 40 instructions a
+// key; two tables for the first digit's counts changed nothing.  One kernel that selects and
+// moves, a head's rows at a time, was slower: 285 us for a copy that this one does in 187.
 #include <string.h>
 
 #include <cooperative_groups.h>
