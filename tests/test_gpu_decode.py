@@ -2,6 +2,7 @@
 head groups, drafted tokens, a shared prefix, collected weights, BF16 and FP8.  Everything
 the operator must not use (unused slots, the rest of a last page) holds NaN."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -294,6 +295,38 @@ def test_two_streams_with_their_own_workspaces():
     torch.cuda.synchronize()
     for x, y in outs:
         assert torch.equal(x, ra) and torch.equal(y, rb)
+
+
+def test_threads_on_streams_of_their_own():
+    """Python threads that call at once, wide batches behind a prefix among them (the prefix's
+    kernel and decode_kernel side by side, twice), get what a call alone gets."""
+    kinds = [dict(lens=[30, 700] * 20, prefix=2000), dict(lens=[3] * 41, prefix=5000), dict(lens=[900, 0, 77], prefix=0)]
+    sets = [Setup(Hq=8, Hkv=2, d=128, seed=30 + i, **k) for i, k in enumerate(kinds)]
+    wss = [S.decode_workspace(s.dec) for s in sets]
+    alone = [s.call(ws=w).clone() for s, w in zip(sets, wss)]
+    outs = [[torch.empty_like(r) for _ in range(20)] for r in alone]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(streams[i]):
+                for o in outs[i]:
+                    s = sets[i]
+                    S.stem_decode(s.dec, s.q, s.cache, s.kv_lens, prefix_table=s.prefix_table, out=o, ws=wss[i])
+        except Exception as e:  # noqa: BLE001  (shown by the assertion)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for i, r in enumerate(alone):
+        assert all(torch.equal(o, r) for o in outs[i])
 
 
 @pytest.mark.parametrize("name", ["gqa4", "q5_gqa4", "prefix_wide", "prefix_wide_fp8", "weights_q4_gqa5", "weights_fp8"])
