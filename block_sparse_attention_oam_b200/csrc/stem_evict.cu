@@ -101,12 +101,20 @@ __device__ __forceinline__ int find_lane(int count, int* left) {
 // share it evenly), their keys in shared memory: warp w takes positions [w, w + 1) * 32 * kpt
 // of it, key e of lane l being number 32 e + l, so that loads are coalesced, no key is another
 // lane's, and ascending order is (warp, e, lane).
+// ONE: a cluster of one CTA (at most 4096 positions), whose joining is a barrier of its own
+// threads and reads of its own bins (1K tokens, with the move 9.6 us a call; 10.0 as a cluster).
+template <bool ONE>
 __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__ EvictParams p) {
   const EvictArgs& a = p.a;
   __shared__ SelectSmem sm;
   extern __shared__ uint32_t keys[];
   cg::cluster_group cluster = cg::this_cluster();
-  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int C = ONE ? 1 : static_cast<int>(cluster.num_blocks()), rank = ONE ? 0 : static_cast<int>(cluster.block_rank());
+  auto join = [&]() {
+    if (ONE) __syncthreads();
+    else cluster.sync();
+  };
+  auto of_rank = [&](int* at, int r) { return ONE ? at : cluster.map_shared_rank(at, r); };
   const int unit = blockIdx.x / C, b = unit / a.Hkv, h = unit % a.Hkv;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const unsigned all = 0xffffffffu;
@@ -199,13 +207,13 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
       sum += __shfl_xor_sync(all, sum, 1);
       sum += __shfl_xor_sync(all, sum, 2);
       if (tid % 4 == 0) sm.coarse[pass][tid / 4] = sum;
-      cluster.sync();
+      join();
       if (pass == 1)  // every CTA has done with pass 0's bins
         for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<int4*>(sm.hist[0])[i] = make_int4(0, 0, 0, 0);
       int got = 0;
 #pragma unroll
       for (int r = tid % 4; r < kMaxCluster; r += 4)
-        if (r < C) got += cluster.map_shared_rank(sm.coarse[pass], r)[kCoarse - 1 - tid / 4];
+        if (r < C) got += of_rank(sm.coarse[pass], r)[kCoarse - 1 - tid / 4];
       got += __shfl_xor_sync(all, got, 1);
       got += __shfl_xor_sync(all, got, 2);
       if (tid % 4 == 0) sm.total[tid / 4] = got;
@@ -221,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
       }
       __syncthreads();
       const int group = sm.group;
-      if (warp < C) sm.fine[warp][lane] = cluster.map_shared_rank(hist, warp)[kFine * group + kFine - 1 - lane];
+      if (warp < C) sm.fine[warp][lane] = of_rank(hist, warp)[kFine * group + kFine - 1 - lane];
       __syncthreads();
       if (warp == 0) {
         int f = 0;
@@ -267,15 +275,17 @@ __global__ void __launch_bounds__(kThreads) evict_select(const __grid_constant__
     sm.counts[0] = all_more;
     sm.counts[1] = all_same;
   }
-  cluster.sync();
+  if (!ONE) {
+    join();
 #pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r)
-    if (r < rank) {
-      const int* c = cluster.map_shared_rank(sm.counts, r);
-      pos += c[0];
-      eq += c[1];
-    }
-  cluster.sync();  // the last look into another CTA's shared memory: each may leave from here on
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < rank) {
+        const int* c = of_rank(sm.counts, r);
+        pos += c[0];
+        eq += c[1];
+      }
+    join();  // the last look into another CTA's shared memory: each may leave from here on
+  }
   // the list, in ascending order; of the equal ones the first `ties`
   const unsigned below = (1u << lane) - 1u;
   pos += min(eq, ties);
@@ -374,9 +384,11 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
   int C = 1;
   while (C < kMaxCluster && C < chunks) C *= 2;
   p.kpt = kMinKeys * ((chunks + C - 1) / C);
-  cudaError_t e = set_smem_once<evict_select>(kMaxKeys * kThreads * 4);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(evict_select, units * C, kThreads, static_cast<size_t>(p.kpt) * kThreads * 4, C, st, p);
+  const size_t smem = static_cast<size_t>(p.kpt) * kThreads * 4;
+  cudaError_t e = C > 1 ? set_smem_once<evict_select<false>>(kMaxKeys * kThreads * 4) : cudaSuccess;
+  if (e == cudaSuccess)
+    e = C > 1 ? launch_dependent(evict_select<false>, units * C, kThreads, smem, C, st, p)
+              : launch_dependent(evict_select<true>, units, kThreads, smem, 1, st, p);
   if (e != cudaSuccess) return e;
   // a move CTA's tokens: 8 pieces a thread, within its table of rows
   const int per_token = 2 * a.Hkv << a.row_shift;

@@ -350,8 +350,9 @@ __device__ __forceinline__ uint32_t e4m3x4_pairsum_h(uint32_t v) {
 __device__ __forceinline__ float2 e4m3x4_pairsum(uint32_t v) { return h2_to_float2(e4m3x4_pairsum_h(v)); }
 
 // Programmatic dependent launch: a kernel launched with launch_dependent may start while
-// its predecessor in the stream still runs; it touches no memory before pdl_wait, which
-// returns when the predecessor has completed.  pdl_trigger lets the successor start.
+// its predecessor in the stream still runs; before pdl_wait, which returns when the predecessor
+// has completed, it touches nothing that the predecessor writes.  pdl_trigger lets the
+// successor start.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
