@@ -811,7 +811,7 @@ __device__ __forceinline__ void load_share(float (&x)[E], const float* src) {
 // Joins the partials of rows whose keys fell to several CTAs (blocks below row_blocks, WPR
 // warps per row: 8, a block for one row, or 1) and adds up the softmax weights (the other blocks, from the stored scores).
 // What follows pdl_wait is latency, so where each row's partials lie is worked out before
-// it, from the lengths (decode_kernel triggers what follows after its own wait, when all that
+// it, from the lengths (what decode_kernel lets go starts after the step's first wait, when all that
 // came before it in the stream is complete), and all loads after it are independent.  Every
 // block waits, those with nothing to join too: what follows in the stream takes this launch's
 // end for decode_kernel's.
