@@ -30,10 +30,11 @@
 // Measured on one B200, whole calls: four ragged BF16 sequences of up to 128K tokens, 32 q- and
 // 8 kv-heads of 128, 216 to 220 us (all of the copy rate); 48 of up to 4K with four new tokens
 // each, 78 us (80 %: the start, and 1 us to join the warps of a unit); one FP8 sequence of 128K,
-// 53 us (77 %: issue slots and the special-function pipe, which converts 64 pairs of codes per
-// warp and tile.  The e4m3 form of the product for S: 55.7.  V's codes shifted into place on
-// the integer pipe: 55.9, and 59 to 63 with the test for NaN codes that it needs.  Tokens as
-// the 128 rows of tcgen05: 67 to 86).
+// 53 us (77 %: twelve consumer warps of 128 registers an SM and their chains of dependent steps;
+// the scheduler issues in 45 % of the cycles, the ALU with the 64 conversions per warp and
+// tile is 44 % busy, the matrix pipe 37 %.  The e4m3 form of the product for S: 55.7.  V's codes
+// shifted into place instead of converted: 55.9, and 59 to 63 with the test for NaN codes that
+// it needs.  Tokens as the 128 rows of tcgen05: 67 to 86).
 // Waits are bounded; on expiry the CTA raises its abort flag, records STEM_ERR_TIMEOUT and
 // runs through the rest of its units without computing.
 #include <string.h>
