@@ -4,6 +4,12 @@ layer and token (stem_decode, stem_evict) a native module, csrc/stem_binding.cpp
 Argument marshalling only: torch tensors provide device memory and the current
 CUDA stream; every step of the path runs in libstem's CUDA kernels.  There is no
 fallback: if the library is missing, every call raises.
+
+A call runs on `stream`, or on the current stream where none is given; its arguments have to be
+ready there, and to live until it has run.  What its caller leaves out (outputs, a workspace) is
+allocated on that stream too.
+A workspace that was left out is gone when the call returns, and with it the status of the call:
+pass one to read it with query_status.
 """
 from __future__ import annotations
 
@@ -227,6 +233,29 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _allocate(device, stream, make) -> torch.Tensor:
+    """make(), a new tensor on `device`, in the order of the call's stream: a workspace's zeroing
+    goes before the kernels, and what is freed when the call returns is used again behind them."""
+    if stream is None:
+        return make()
+    if stream.device != device:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _output(device, stream, shape, dtype) -> torch.Tensor:
+    """An output that the caller left out.  Its current stream may read it and let go of it there."""
+    t = _allocate(device, stream, lambda: torch.empty(shape, dtype=dtype, device=device))
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _workspace(prob: Problem, device, ws, stream):
+    return _allocate(device, stream, lambda: workspace(prob, device)) if ws is None else ws
+
+
 def _paged(paged: Optional[PagedKV]):
     return None if paged is None else paged.c()
 
@@ -247,21 +276,26 @@ def workspace(prob: Problem, device="cuda") -> torch.Tensor:
 def stem_score(prob: Problem, q, k, v, paged: Optional[PagedKV] = None, scores=None, ws=None, stream=None):
     sz = prob.sizes()
     if scores is None:
-        scores = torch.empty((prob.num_q_heads, sz["scores_per_head"]), dtype=torch.float32, device=q.device)
-    ws = workspace(prob, q.device) if ws is None else ws
+        scores = _output(q.device, stream, (prob.num_q_heads, sz["scores_per_head"]), torch.float32)
+    ws = _workspace(prob, q.device, ws, stream)
     _check(lib().stem_score(prob.c, _ptr(q), _ptr(k), _ptr(v), _paged(paged), _ptr(scores), _ptr(ws),
                             ws.numel(), _stream(stream)))
     return scores
 
 
+def _lists(sz, dev, row_ptr, col_idx, stream):
+    if row_ptr is None:
+        row_ptr = _output(dev, stream, sz["num_rows"] + 1, torch.int32)
+    if col_idx is None:
+        col_idx = _output(dev, stream, (sz["list_heads"], sz["nnz_per_head"]), torch.int32)
+    return row_ptr, col_idx
+
+
 def stem_select(prob: Problem, scores, row_ptr=None, col_idx=None, ws=None, stream=None):
     sz = prob.sizes()
     dev = scores.device
-    if row_ptr is None:
-        row_ptr = torch.empty(sz["num_rows"] + 1, dtype=torch.int32, device=dev)
-    if col_idx is None:
-        col_idx = torch.empty((sz["list_heads"], sz["nnz_per_head"]), dtype=torch.int32, device=dev)
-    ws = workspace(prob, dev) if ws is None else ws
+    row_ptr, col_idx = _lists(sz, dev, row_ptr, col_idx, stream)
+    ws = _workspace(prob, dev, ws, stream)
     _check(lib().stem_select(prob.c, _ptr(scores), _ptr(row_ptr), _ptr(col_idx), _ptr(ws), ws.numel(),
                              _stream(stream)))
     return row_ptr, col_idx
@@ -272,26 +306,23 @@ def stem_score_select(prob: Problem, q, k, v, paged: Optional[PagedKV] = None, r
     """Pool, score and select in one pass (no score matrix): returns (row_ptr, col_idx)."""
     sz = prob.sizes()
     dev = q.device
-    if row_ptr is None:
-        row_ptr = torch.empty(sz["num_rows"] + 1, dtype=torch.int32, device=dev)
-    if col_idx is None:
-        col_idx = torch.empty((sz["list_heads"], sz["nnz_per_head"]), dtype=torch.int32, device=dev)
-    ws = workspace(prob, dev) if ws is None else ws
+    row_ptr, col_idx = _lists(sz, dev, row_ptr, col_idx, stream)
+    ws = _workspace(prob, dev, ws, stream)
     _check(lib().stem_score_select(prob.c, _ptr(q), _ptr(k), _ptr(v), _paged(paged), _ptr(row_ptr), _ptr(col_idx),
                                    _ptr(ws), ws.numel(), _stream(stream)))
     return row_ptr, col_idx
 
 
-def _out(prob, q, out):
+def _out(prob, q, out, stream=None):
     if out is None:
-        out = torch.empty((q.shape[0], prob.num_q_heads, prob.head_dim), dtype=torch.bfloat16, device=q.device)
+        out = _output(q.device, stream, (q.shape[0], prob.num_q_heads, prob.head_dim), torch.bfloat16)
     return out
 
 
 def bsa_prefill(prob: Problem, q, k, v, row_ptr, col_idx, paged: Optional[PagedKV] = None, out=None, lse=None,
                 ws=None, stream=None):
-    out = _out(prob, q, out)
-    ws = workspace(prob, q.device) if ws is None else ws
+    out = _out(prob, q, out, stream)
+    ws = _workspace(prob, q.device, ws, stream)
     _check(lib().bsa_prefill(prob.c, _ptr(q), _ptr(k), _ptr(v), _paged(paged), _ptr(row_ptr), _ptr(col_idx),
                              _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
     return out
@@ -299,8 +330,8 @@ def bsa_prefill(prob: Problem, q, k, v, row_ptr, col_idx, paged: Optional[PagedK
 
 def bsa_dense_prefill(prob: Problem, q, k, v, paged: Optional[PagedKV] = None, out=None, lse=None, ws=None,
                       stream=None):
-    out = _out(prob, q, out)
-    ws = workspace(prob, q.device) if ws is None else ws
+    out = _out(prob, q, out, stream)
+    ws = _workspace(prob, q.device, ws, stream)
     _check(lib().bsa_dense_prefill(prob.c, _ptr(q), _ptr(k), _ptr(v), _paged(paged), _ptr(out), _ptr(lse),
                                    _ptr(ws), ws.numel(), _stream(stream)))
     return out
@@ -308,8 +339,8 @@ def bsa_dense_prefill(prob: Problem, q, k, v, paged: Optional[PagedKV] = None, o
 
 def stem_attention(prob: Problem, q, k, v, paged: Optional[PagedKV] = None, out=None, lse=None, row_ptr=None,
                    col_idx=None, ws=None, stream=None):
-    out = _out(prob, q, out)
-    ws = workspace(prob, q.device) if ws is None else ws
+    out = _out(prob, q, out, stream)
+    ws = _workspace(prob, q.device, ws, stream)
     _check(lib().stem_attention(prob.c, _ptr(q), _ptr(k), _ptr(v), _paged(paged), _ptr(out), _ptr(lse),
                                 _ptr(row_ptr), _ptr(col_idx), _ptr(ws), ws.numel(), _stream(stream)))
     return out
@@ -343,13 +374,13 @@ def stem_attention_host(prob: Problem, q_host, k_host, v_host, q, k, v, paged: O
     q / k / v / out (a paged cache: paged.k_cache / paged.v_cache) are device scratch
     of the full sizes, overwritten with the inputs staged group by group.  Returns
     out_host; the work is asynchronous on `stream` (synchronise before reading it)."""
-    out = _out(prob, q, out)
+    out = _out(prob, q, out, stream)
     if out_host is None:
         out_host = torch.empty(tuple(out.shape), dtype=torch.bfloat16, pin_memory=True)
     for t, name in ((q_host, "q_host"), (k_host, "k_host"), (v_host, "v_host"), (out_host, "out_host")):
         if t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous host tensor")
-    ws = workspace(prob, q.device) if ws is None else ws
+    ws = _workspace(prob, q.device, ws, stream)
     _check(lib().stem_attention_host(prob.c, _ptr(q_host), _ptr(k_host), _ptr(v_host), _ptr(q), _ptr(k), _ptr(v),
                                      _paged(paged), _ptr(out_host), _ptr(out), _ptr(lse), _ptr(row_ptr),
                                      _ptr(col_idx), int(out_groups), _ptr(ws), ws.numel(), _stream(stream)))
@@ -361,7 +392,7 @@ def stem_attention_noalloc(prob: Problem, q, k, v, paged: Optional[PagedKV] = No
     """stem_attention with the library's static scratch instead of a workspace
     (for callers that cannot allocate device memory).  `status`: optional device
     int32 tensor of one element that receives the call's device status word."""
-    out = _out(prob, q, out)
+    out = _out(prob, q, out, stream)
     _check(lib().stem_attention_noalloc(prob.c, _ptr(q), _ptr(k), _ptr(v), _paged(paged), _ptr(out), _ptr(lse),
                                         _ptr(row_ptr), _ptr(col_idx), _ptr(status), _stream(stream)))
     return out
@@ -462,9 +493,9 @@ def stem_decode(dec: Decode, q, cache: PagedKV, kv_lens, prefix_table=None, weig
     if dev.type != "cuda":
         raise ValueError("stem_decode takes CUDA tensors")
     if out is None:
-        out = torch.empty((B * n, Hq, d), dtype=torch.bfloat16, device=dev)
+        out = _output(dev, stream, (B * n, Hq, d), torch.bfloat16)
     if ws is None:
-        ws = decode_workspace(dec, dev)
+        ws = _allocate(dev, stream, lambda: decode_workspace(dec, dev))
     if dec.weights != (weights_out is not None) or (weights_in is not None and weights_out is None):
         raise ValueError("weights_out goes with Decode(weights=True), weights_in with weights_out")
     call, entry, _, _ = _native or _binding()
@@ -535,11 +566,11 @@ def stem_evict(ev: Evict, src: PagedKV, kv_lens, weights, dst: PagedKV, kv_lens_
     if dev.type != "cuda":
         raise ValueError("stem_evict takes CUDA tensors")
     if kv_lens_out is None:
-        kv_lens_out = torch.empty(B, dtype=torch.int32, device=dev)
+        kv_lens_out = _output(dev, stream, B, torch.int32)
     if keep is None:
-        keep = torch.empty((B, Hkv, ev.budget), dtype=torch.int32, device=dev)
+        keep = _output(dev, stream, (B, Hkv, ev.budget), torch.int32)
     if ws is None:
-        ws = evict_workspace(ev, dev)
+        ws = _allocate(dev, stream, lambda: evict_workspace(ev, dev))
     _, _, call, entry = _native or _binding()
     status = call(entry, ev._c, weights, src.k_cache, src.v_cache, src.block_table, dst.k_cache, dst.v_cache,
                   dst.block_table, kv_lens, kv_lens_out, weights_out, keep, ws,
