@@ -25,8 +25,12 @@
 //     128-row tcgen05 tile would hold 4 rows here, and its softmax would still be
 //     one thread per row.
 //   - FP8: K and V codes are widened to f16 in registers, which is exact, and P is rounded
-//     to f16 (2^-11), not to e4m3.  BF16: P is rounded to bf16 (2^-8), as V is;
-//     the sums l are those of the unrounded p.
+//     to f16 (2^-11), not to e4m3.  f16's normal range ends at 2^-14, and a long tail of small
+//     weights has to count; so p is taken as 2^(s - m + kLift): its largest entry is at least 2^7,
+//     and at most 2^15 by the running maximum's slack, and what is below the normal range is off
+//     by 2^-32 of the largest weight at most.  BF16: P is rounded to bf16 (2^-8), the type
+//     of V, which the matrix instruction wants in both; it has float32's range.
+//     The sums l are those of the unrounded p.
 // Measured on one B200, whole calls: four ragged BF16 sequences of up to 128K tokens, 32 q- and
 // 8 kv-heads of 128, 216 to 220 us (all of the copy rate); 48 of up to 4K with four new tokens
 // each, 78 us (80 %: the start, and 1 us to join the warps of a unit); one FP8 sequence of 128K,
@@ -63,6 +67,7 @@ struct Cfg {
   // and per byte twice the work, which is latency and wants more warps
   static constexpr int CTAS = STAGE == 32 * 1024 ? 2 : 3;
   static constexpr int NST = 3;
+  static constexpr float kLift = FP8 ? kLiftF16 : 0.f;
   static constexpr int MROWS = 512 / D;             // rows joined in one round
   static constexpr int MSTRIDE = D + 8;             // floats: the rows' banks apart
   static constexpr int MERGE = 4 * MROWS * MSTRIDE * 4;  // of four warps
@@ -528,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) decode_kernel(con
             acc[i][3] *= a1;
           }
         }
-        const float u0 = m0 == -INFINITY ? 0.f : m0;
+        const float u0 = m0 == -INFINITY ? 0.f : m0 - C::kLift;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           s[j][0] = ex2_approx(s[j][0] - u0);
@@ -536,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) decode_kernel(con
         }
         l0 += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
         if (upper_rows) {
-          const float u1 = m1 == -INFINITY ? 0.f : m1;
+          const float u1 = m1 == -INFINITY ? 0.f : m1 - C::kLift;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             s[j][2] = ex2_approx(s[j][2] - u1);
@@ -625,8 +630,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) decode_kernel(con
     l0 += __shfl_xor_sync(all, l0, 2);
     l1 += __shfl_xor_sync(all, l1, 2);
     if (qd == 0) {
-      ml[warp * 16 + r0] = make_float2(m0, l0);
-      ml[warp * 16 + r0 + 8] = make_float2(m1, l1);
+      ml[warp * 16 + r0] = make_float2(m0 - C::kLift, l0);
+      ml[warp * 16 + r0 + 8] = make_float2(m1 - C::kLift, l1);
     }
     const bool direct = was.own && was.p0 == 0 && was.p1 == was.pages && a.prefix_len == 0;
     const long long slot = static_cast<long long>(gang_no + was.unit) * p.gang + rank;

@@ -25,7 +25,8 @@
 // last product.  Tiles of 64 keys with a second S took 95 us where these took 85.
 // Measured on one B200, whole calls, 32 q- and 8 kv-heads of 128: 64 sequences of up to 1K own
 // tokens behind 32768 shared ones, BF16, 73 to 80 us; 128 of up to 512 behind 16384, FP8, 72 us.
-// BF16 rounds P to bf16, as V is.  V rows behind the prefix's end (the rest of its last page)
+// P in f16 is taken as 2^(s - m + 7), as in decode_kernel, so that a long tail of small weights
+// counts; BF16 rounds P to bf16, as V is.  V rows behind the prefix's end (the rest of its last page)
 // are set to zero in shared memory, since they may hold NaN and 0 * NaN is not 0.
 // Waits are bounded as in the other kernels.
 #include <string.h>
@@ -59,6 +60,7 @@ struct Cfg {
   static constexpr int OFF_MAX = OFF_BAR + 512;     // float [2][2 slots][2 halves][128 rows]
   static constexpr int SMEM = OFF_MAX + 4096 + 1024;
   static_assert(SMEM <= 227 * 1024 && SMEM > 114 * 1024, "one CTA per SM");
+  static constexpr float kLift = FP8 ? kLiftF16 : 0.f;
   static constexpr int THREADS = 32 * (FP8 ? 20 : 18);
   static constexpr int S_STEPS = D * ES / 32;
   static constexpr int PV_STEPS = kBN / 16;
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1) prefix_kernel(const _
         const bool resc = m_new > m_run + 8.0f;
         const float m_use = resc ? m_new : m_run;
         const float alpha = resc ? ex2_approx(m_run - m_use) : 1.0f;
-        const float m_sub = m_use == -INFINITY ? 0.f : m_use;
+        const float m_sub = m_use == -INFINITY ? 0.f : m_use - C::kLift;
         const float2 bias2 = make_float2(-m_sub, -m_sub);
         float2 sq[4];
 #pragma unroll
@@ -519,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1) prefix_kernel(const _
           for (int e = 0; e < 32; e += 8) st_global32(out + c * 32 + e, &o[e]);
         }
       }
-      if (half == 0 && r < rows) p.part_ml[row] = make_float2(m_run, l + l_other);
+      if (half == 0 && r < rows) p.part_ml[row] = make_float2(m_run - C::kLift, l + l_other);
       tc_fence_before();
     }
   } else {

@@ -478,6 +478,10 @@ constexpr int kDecodeRows = 16;       // query rows of a unit
 // that many empty ones on the line, so that a CTA with many short sequences gets fewer.
 constexpr int kDecodeUnitCost = 4;
 
+// P in f16 is 2^(s - m + kLiftF16): with a running maximum m that lags by 8 at most it stays
+// within 2^15, and keys down to 2^-21 of the largest weight (2^-14 without it) keep f16's 2^-11.
+constexpr float kLiftF16 = 7.f;
+
 // The kv-heads that CTAs walk side by side: neighbours in memory (a page of one head is 64
 // pieces of 128 or 256 bytes), so that they read whole DRAM rows between them.
 inline int gang_of(int Hkv) {
