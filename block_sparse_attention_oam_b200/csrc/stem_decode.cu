@@ -519,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) decode_kernel(con
           x1 = fmaxf(x1, __shfl_xor_sync(all, x1, 2));
         }
         if (__any_sync(all, x0 > m0 + 8.0f || x1 > m1 + 8.0f)) {
-          const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+          // each row by its own scores alone: a prefix's rows are several sequences'
+          const float n0 = x0 > m0 + 8.0f ? x0 : m0, n1 = x1 > m1 + 8.0f ? x1 : m1;
           const float a0 = n0 == m0 ? 1.0f : ex2_approx(m0 - n0), a1 = n1 == m1 ? 1.0f : ex2_approx(m1 - n1);
           m0 = n0;
           m1 = n1;

@@ -319,7 +319,8 @@ STEM_API size_t stem_decode_workspace_size(const stem_decode_t* dec);
  * ws: DEVICE workspace of ws_bytes >= stem_decode_workspace_size(), its first 256 bytes
  *   zero before its first use (stem_reset_status).  Calls that may overlap on the GPU
  *   (other streams, graphs replayed side by side) each need a workspace of their own.
- * Sums and softmax statistics are float32; the result does not depend on timing.
+ * Sums and softmax statistics are float32; a sequence's result does not depend on timing, nor,
+ * sizes and lengths given, on what the other sequences hold.
  */
 STEM_API stem_status_t stem_decode(const stem_decode_t* dec, const void* q, const stem_paged_kv_t* cache,
                                    const int32_t* kv_lens, const int32_t* prefix_table, const float* weights_in,

@@ -1,4 +1,5 @@
-"""stem_decode's numbers where they are hardest to hold: a long even tail under one dominant key."""
+"""stem_decode's numbers where they are hardest to hold: a long even tail under one dominant key,
+and sequences beside one that holds huge values and NaN."""
 import math
 
 import numpy as np
@@ -6,6 +7,8 @@ import pytest
 import torch
 
 from block_sparse_attention_oam_b200 import stem as S
+from tests import test_gpu_decode as D
+
 pytestmark = pytest.mark.gpu
 
 PAGE = S.PAGE_SIZE
@@ -79,3 +82,41 @@ def test_a_long_tail_under_a_dominant_key(name, below):
     assert err <= bound, f"{err} against {bound}, of {ref}"
     ref_lse = top + math.log1p(tail)
     assert (lse.double() - ref_lse).abs().max().item() <= 2 * e
+
+
+GROUPS = {
+    "own": dict(lens=[300, 65, 700, 9], Hq=8, Hkv=2, d=128, weights=True),
+    "own_q3": dict(lens=[300, 65, 700, 9], Hq=8, Hkv=2, d=128, q_len=3),
+    "narrow_prefix": dict(lens=[30, 65, 0, 9], Hq=8, Hkv=2, d=128, prefix=1000, weights=True),
+    "narrow_prefix_d64": dict(lens=[30, 65, 0, 9], Hq=8, Hkv=2, d=64, prefix=1000),
+    "narrow_prefix_fp8": dict(lens=[30, 65, 0, 9], Hq=8, Hkv=2, d=128, prefix=1000, dtype="fp8_e4m3"),
+    "wide_prefix": dict(lens=[30, 65, 0, 9] * 10, Hq=8, Hkv=2, d=128, prefix=1000, weights=True),
+    "wide_prefix_fp8": dict(lens=[30, 65, 0, 9] * 10, Hq=8, Hkv=2, d=128, prefix=1000, dtype="fp8_e4m3"),
+}
+
+
+@pytest.mark.parametrize("hold", ["large", "nan"])
+@pytest.mark.parametrize("name", list(GROUPS))
+def test_a_sequence_leaves_the_others_alone(name, hold):
+    """Other queries, keys and values of one sequence, the lengths as they were (so that the work
+    is split as before): every other sequence's output, log-sum-exp and weights keep their bits."""
+    s = D.Setup(seed=60, **GROUPS[name])
+    ws = S.decode_workspace(s.dec)
+    want = s.call(ws=ws).clone()
+    want_lse, want_w = s.lse.clone(), s.w_out.clone() if s.weights else None
+    changed = 1
+    x = torch.full((s.d,), float("nan") if hold == "nan" else 400.0, device="cuda").to(s.q.dtype).view(torch.uint8)
+    s.q.view(torch.uint8)[changed * s.n: (changed + 1) * s.n] = x
+    n = s.lens[changed]
+    for p in range(-(-n // PAGE)):
+        slot = int(s.cache.block_table[changed, p])
+        for c in (s.cache.k_cache, s.cache.v_cache):
+            c.view(torch.uint8)[slot, : min(PAGE, n - p * PAGE)] = x
+    got = s.call(ws=ws)
+    rows = [r for r in range(len(s.lens) * s.n) if r // s.n != changed]
+    assert torch.equal(got[rows], want[rows])
+    assert torch.equal(s.lse[:, rows], want_lse[:, rows])
+    if s.weights:
+        others = [b for b in range(len(s.lens)) if b != changed]
+        assert torch.equal(s.w_out[others], want_w[others])
+    assert not torch.equal(got[changed * s.n: (changed + 1) * s.n], want[changed * s.n: (changed + 1) * s.n])
