@@ -398,10 +398,11 @@ def stem_attention_noalloc(prob: Problem, q, k, v, paged: Optional[PagedKV] = No
     return out
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True)
 class Decode:
     """One decoding step: the newest q_len tokens of num_seqs sequences over a paged cache
-    (stem_decode_t).  The numbers are taken when the object is made."""
+    (stem_decode_t).  Not to be changed: dataclasses.replace makes one of other numbers (the scale
+    of a step's queries, say)."""
     num_seqs: int
     num_q_heads: int
     num_kv_heads: int
@@ -417,10 +418,11 @@ class Decode:
     weights: bool = False        # also add up the softmax weights of every cached token
 
     def __post_init__(self):
-        self._c = _Decode(self.num_seqs, self.q_len, self.num_q_heads, self.num_kv_heads, self.head_dim,
-                          _dtype_code(self.dtype), self.q_scale, self.k_scale, self.v_scale, self.softmax_scale,
-                          self.max_kv_len, self.prefix_len, 1 if self.weights else 0)
-        self._torch = _TORCH_DTYPES[self.dtype]
+        c = _Decode(self.num_seqs, self.q_len, self.num_q_heads, self.num_kv_heads, self.head_dim,
+                    _dtype_code(self.dtype), self.q_scale, self.k_scale, self.v_scale, self.softmax_scale,
+                    self.max_kv_len, self.prefix_len, 1 if self.weights else 0)
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_torch", _TORCH_DTYPES[self.dtype])
 
     @property
     def c(self):
@@ -522,10 +524,10 @@ def stem_decode(dec: Decode, q, cache: PagedKV, kv_lens, prefix_table=None, weig
     return out
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True)
 class Evict:
-    """One eviction: every (sequence, kv-head) cut to `budget` tokens (stem_evict_t).  The
-    numbers are taken when the object is made."""
+    """One eviction: every (sequence, kv-head) cut to `budget` tokens (stem_evict_t).  Not to
+    be changed, as Decode."""
     num_seqs: int
     num_kv_heads: int
     head_dim: int
@@ -536,9 +538,10 @@ class Evict:
     dtype: str = "bf16"
 
     def __post_init__(self):
-        self._c = _Evict(self.num_seqs, self.num_kv_heads, self.head_dim, _dtype_code(self.dtype), self.max_kv_len,
-                         self.budget, self.sink, self.recent)
-        self._torch = _TORCH_DTYPES[self.dtype]
+        c = _Evict(self.num_seqs, self.num_kv_heads, self.head_dim, _dtype_code(self.dtype), self.max_kv_len,
+                   self.budget, self.sink, self.recent)
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_torch", _TORCH_DTYPES[self.dtype])
 
     @property
     def c(self):
