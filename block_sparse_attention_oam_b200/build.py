@@ -6,6 +6,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -37,12 +38,25 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def binding_tag() -> str:
+    """What the native module is built against; the module holds it as a string."""
+    import torch
+
+    return f"stem_binding for torch {torch.__version__}, Python {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_fits() -> bool:
+    """Whether the module was built against this torch and Python: it uses torch's C++
+    classes, so another's must not even be loaded."""
+    with open(BINDING, "rb") as f:
+        return binding_tag().encode() + b"\0" in f.read()
+
+
 def build_binding(force: bool = False) -> str:
     deps = [BINDING_SRC, os.path.join(ROOT, "include", "stem.h")]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+    if (not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps)
+            and binding_fits()):
         return BINDING
-    import sysconfig
-
     import torch
 
     home = os.path.dirname(torch.__file__)
@@ -50,7 +64,7 @@ def build_binding(force: bool = False) -> str:
     dirs = [os.path.join(home, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
             os.path.join(ROOT, "include")]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{d}" for d in dirs), BINDING_SRC,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DSTEM_BINDING_TAG="{binding_tag()}"', *(f"-I{d}" for d in dirs), BINDING_SRC,
            "-o", BINDING + ".tmp", "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -193,4 +193,7 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "stem_binding", nullptr, -1, kMeth
 
 }  // namespace
 
+// What this was built against, looked for in the file before it is loaded.
+extern "C" __attribute__((used, visibility("default"))) const char stem_binding_tag[] = STEM_BINDING_TAG;
+
 PyMODINIT_FUNC PyInit_stem_binding() { return PyModule_Create(&kModule); }

@@ -23,6 +23,8 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
+from . import build
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libstem.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "stem.h")
@@ -466,12 +468,14 @@ _native = None
 
 
 def _binding():
-    """The native module and libstem's entry points for it.  Raises if it is missing."""
+    """The native module and libstem's entry points for it.  Raises if it is missing, or built
+    for another torch or Python."""
     global _native
     if _native is None:
-        path = os.path.join(_PKG, "stem_binding.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with `python -m block_sparse_attention_oam_b200.build`")
+        path = build.BINDING
+        if not os.path.exists(path) or not build.binding_fits():
+            why = "built for another torch or Python" if os.path.exists(path) else "missing"
+            raise RuntimeError(f"{path} is {why}: build it with `python -m block_sparse_attention_oam_b200.build`")
         spec = importlib.util.spec_from_file_location("stem_binding", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
