@@ -353,7 +353,8 @@ def capture_attention(prob: Problem, q, k, v, paged: Optional[PagedKV] = None, o
     """Capture one stem_attention call (pooling, scoring, selection, BSA: every kernel of
     the path) into a CUDA graph on these buffers.  `graph.replay()` re-runs the whole path
     on whatever the buffers hold at replay time, with one launch from the host.  The
-    problem (sequence lengths, heads, knobs) is fixed by the capture.  Returns (graph, out)."""
+    problem (sequence lengths, heads, knobs) is fixed by the capture.  Returns (graph, out); the
+    buffers have to live as long as the graph, which holds the workspace (graph.workspace)."""
     out = _out(prob, q, out)
     ws = workspace(prob, q.device) if ws is None else ws
     side = torch.cuda.Stream(device=q.device)
@@ -364,6 +365,7 @@ def capture_attention(prob: Problem, q, k, v, paged: Optional[PagedKV] = None, o
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         stem_attention(prob, q, k, v, paged, out, lse, row_ptr, col_idx, ws)
+    graph.workspace = ws  # every replay writes it
     return graph, out
 
 

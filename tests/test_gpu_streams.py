@@ -65,3 +65,19 @@ def test_prefill():
     assert all(torch.equal(x, want) for x in got)
     got = _beside(lambda side: S.stem_score_select(prob, dev["q"], dev["k"], dev["v"], stream=side), sizes + [rp.numel() * 4, ci.numel() * 4])
     assert all(torch.equal(a, rp) and torch.equal(b, ci) for a, b in got)
+
+
+def test_a_captured_path_leaves_other_memory_alone():
+    """A captured path that made its own workspace: what is allocated afterwards is not its to write."""
+    wl = W.QWEN_32K.with_(name="captured_alone", seqlens=(2048, 700), num_q_heads=8, num_kv_heads=2, seed=53)
+    inp = W.make_inputs(wl)
+    prob, dev = S.problem_for(wl, inp), T.to_device(inp)
+    want = S.stem_attention(prob, dev["q"], dev["k"], dev["v"])
+    graph, out = S.capture_attention(prob, dev["q"], dev["k"], dev["v"])
+    n = prob.sizes()["workspace_bytes"]
+    held = [torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
+    assert all((t == 0xA5).all() for t in held)

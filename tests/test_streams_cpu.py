@@ -1,6 +1,8 @@
 """Where a call with a stream of its own allocates what its caller left out, seen without a GPU:
 the allocator, the streams and the library are stand-ins that write down what happens."""
 import contextlib
+import gc
+import weakref
 
 import pytest
 import torch
@@ -131,3 +133,29 @@ def test_a_stream_of_another_device_is_refused(log, monkeypatch, name):
     with pytest.raises(ValueError, match="cuda:1"):
         calls(log, monkeypatch)[name](Stream("elsewhere", torch.device("cuda", 1)))
     assert not log.calls
+
+
+def test_a_captured_path_keeps_its_workspace(log, monkeypatch):
+    """Replays write the workspace, so it lives as long as the graph, given or not."""
+    @contextlib.contextmanager
+    def on(stream):
+        yield
+
+    class Graph:
+        pass
+
+    side = Stream("the first call's")
+    side.wait_stream = lambda s: None
+    log.mine.wait_stream = lambda s: None
+    monkeypatch.setattr(torch.cuda, "Stream", lambda device=None: side)
+    monkeypatch.setattr(torch.cuda, "CUDAGraph", Graph)
+    monkeypatch.setattr(torch.cuda, "graph", on)
+    graph, _ = S.capture_attention(_problem(monkeypatch), log.t, log.t, log.t)
+    ws, = [weakref.ref(t) for t in log.made if t.how == "zeros"]
+    log.made.clear()
+    log.calls.clear()
+    gc.collect()
+    assert ws() is not None
+    del graph
+    gc.collect()
+    assert ws() is None
