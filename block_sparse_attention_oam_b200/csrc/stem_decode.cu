@@ -681,9 +681,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) decode_kernel(con
           const int g = row_base + r;
           const int tok = div_g(p, g);
           const int h = was.kvh * G + g - tok * G;
-          const float inv = M == -INFINITY && L == 0.f ? 0.f : a.v_scale / L;  // nothing seen: o = 0
+          const float inv = M == -INFINITY && L == 0.f ? 0.f : 1.0f / L;  // nothing seen: o = 0
           *reinterpret_cast<uint2*>(static_cast<unsigned char*>(a.out) + ((static_cast<long long>(tok) * a.Hq + h) * D + col) * 2) =
-              make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+              make_uint2(pack_bf16x2(o.x * inv * a.v_scale, o.y * inv * a.v_scale),
+                         pack_bf16x2(o.z * inv * a.v_scale, o.w * inv * a.v_scale));
           if (a.lse != nullptr && col == 0)
             a.lse[static_cast<long long>(h) * a.B * a.n + tok] =
                 L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
@@ -886,11 +887,11 @@ __global__ void __launch_bounds__(kFinishThreads, 3) decode_finish(const __grid_
 #pragma unroll
           for (int e = 0; e < E; ++e) o[e] += shares[(tid + 32 * y) * E + e];
       }
-      const float inv = st.x == -INFINITY && st.y == 0.f ? 0.f : a.v_scale / st.y;
+      const float inv = st.x == -INFINITY && st.y == 0.f ? 0.f : 1.0f / st.y;
       uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.out) +
                                                   ((static_cast<long long>(tok) * a.Hq + h) * D + lane * E) * 2);
 #pragma unroll
-      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(o[e] * inv * a.v_scale, o[e + 1] * inv * a.v_scale);
       if (a.lse != nullptr && lane == 0)
         a.lse[static_cast<long long>(h) * a.B * a.n + tok] =
             st.y == 0.f ? -INFINITY : (st.x + log2f(st.y)) * 0.69314718055994531f;

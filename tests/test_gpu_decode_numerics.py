@@ -84,6 +84,22 @@ def test_a_long_tail_under_a_dominant_key(name, below):
     assert (lse.double() - ref_lse).abs().max().item() <= 2 * e
 
 
+@pytest.mark.parametrize("v_scale", [1.6e-39, 1e35])
+@pytest.mark.parametrize("B,prefix", [(1, 0), (500, 0), (60, 65001)])
+def test_value_scales_at_the_ends_of_float32(v_scale, B, prefix):
+    """A mean of 64K equal values, joined from many CTAs' shares or within one: all operations
+    between are relative errors of 2^-20 at most, the output's rounding 2^-8."""
+    table = torch.zeros((B, 1024), dtype=torch.int32, device="cuda")
+    e4 = torch.float8_e4m3fn
+    kv = S.PagedKV(torch.zeros((1, PAGE, 1, 128), device="cuda").to(e4), torch.full((1, PAGE, 1, 128), 8.0, device="cuda").to(e4), table)
+    dec = S.Decode(B, 1, 1, 128, max_kv_len=65536, dtype="fp8_e4m3", v_scale=v_scale, prefix_len=prefix)
+    lens = torch.full((B,), 0 if prefix else 65536, dtype=torch.int32, device="cuda")
+    ptable = torch.zeros(-(-prefix // PAGE), dtype=torch.int32, device="cuda") if prefix else None
+    out = S.stem_decode(dec, torch.ones((B, 1, 128), device="cuda").to(e4), kv, lens, prefix_table=ptable)
+    want = 8 * float(np.float32(v_scale))
+    assert ((out.double() / want - 1).abs() <= 2.0 ** -8 * 1.01).all()
+
+
 GROUPS = {
     "own": dict(lens=[300, 65, 700, 9], Hq=8, Hkv=2, d=128, weights=True),
     "own_q3": dict(lens=[300, 65, 700, 9], Hq=8, Hkv=2, d=128, q_len=3),
