@@ -1,6 +1,6 @@
 // Entry points of the decoding operators declared in include/stem.h: argument checks,
 // workspace layout, and the launches.
-#include <math.h>
+#include <float.h>
 
 #include <cmath>
 
@@ -47,6 +47,13 @@ stem_status_t check_cache(const stem_paged_kv_t* c, const char* what, int max_le
   return STEM_OK;
 }
 
+// sigma q_scale k_scale log2(e), what a product of codes (or BF16 values) is multiplied by
+double score_scale(const stem_decode_t* de) {
+  const double sigma = de->softmax_scale > 0.f ? de->softmax_scale : 1.0 / std::sqrt(static_cast<double>(de->head_dim));
+  const double codes = de->dtype == STEM_DT_FP8_E4M3 ? static_cast<double>(de->q_scale) * de->k_scale : 1.0;
+  return sigma * codes * 1.4426950408889634;
+}
+
 stem_status_t check_decode(const stem_decode_t* de) {
   if (de == nullptr) return set_last_error(STEM_ERR_INVALID, "decode problem is NULL");
   stem_status_t s = check_shape(de->num_seqs, de->num_kv_heads, de->head_dim, de->dtype, de->max_kv_len);
@@ -62,6 +69,8 @@ stem_status_t check_decode(const stem_decode_t* de) {
         !std::isfinite(de->k_scale) || !std::isfinite(de->v_scale))
       return set_last_error(STEM_ERR_INVALID, "FP8 scales must be finite and positive");
   if (!std::isfinite(de->softmax_scale)) return set_last_error(STEM_ERR_INVALID, "softmax_scale is not finite");
+  if (score_scale(de) > FLT_MAX)
+    return set_last_error(STEM_ERR_INVALID, "softmax_scale x q_scale x k_scale is beyond float32");
   if (de->prefix_len < 0 || de->prefix_len > STEM_MAX_KV_LEN)
     return set_last_error(STEM_ERR_INVALID, "prefix_len %d outside [0, %d]", de->prefix_len, STEM_MAX_KV_LEN);
   if (de->collect_weights != 0 && de->collect_weights != 1)
@@ -168,8 +177,6 @@ stem_status_t stem_decode(const stem_decode_t* dec, const void* q, const stem_pa
   const DecodeWs w = layout(dec);
   if ((s = check_ws(ws, ws_bytes, w.total)) != STEM_OK) return s;
   const bool fp8 = dec->dtype == STEM_DT_FP8_E4M3;
-  const float sigma =
-      dec->softmax_scale > 0.f ? dec->softmax_scale : 1.0f / sqrtf(static_cast<float>(dec->head_dim));
   DecodeArgs a{};
   a.q = q;
   a.kv_lens = kv_lens;
@@ -187,7 +194,7 @@ stem_status_t stem_decode(const stem_decode_t* dec, const void* q, const stem_pa
   a.d = dec->head_dim;
   a.max_kv_len = dec->max_kv_len;
   a.prefix_len = dec->prefix_len;
-  a.scale_log2 = sigma * (fp8 ? dec->q_scale * dec->k_scale : 1.0f) * 1.4426950408889634f;
+  a.scale_log2 = static_cast<float>(score_scale(dec));
   a.v_scale = fp8 ? dec->v_scale : 1.0f;
   a.weights_in = weights_in;
   a.weights_out = weights_out;

@@ -285,7 +285,7 @@ typedef struct {
   int head_dim;                /* d: 64 or 128 (FP8: 128) */
   stem_dtype_t dtype;          /* storage type of Q and of the cache */
   float q_scale, k_scale, v_scale; /* FP8: value = code * scale (per tensor); BF16: ignored */
-  float softmax_scale;         /* sigma; <= 0 selects 1/sqrt(head_dim) */
+  float softmax_scale;         /* sigma; <= 0 selects 1/sqrt(head_dim); sigma q_scale k_scale log2(e) within float32 */
   int max_kv_len;              /* no kv_lens entry exceeds it; 1..STEM_MAX_KV_LEN */
   int prefix_len;              /* tokens of a prefix that all sequences share, 0: none; at most STEM_MAX_KV_LEN */
   int collect_weights;         /* 1: also add up the softmax weights each cached token receives */
