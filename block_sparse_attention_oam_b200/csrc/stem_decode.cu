@@ -5,10 +5,11 @@
 // kept as (m, l = sum p, O = sum p v) so that shares of the keys computed apart can be
 // joined: with M = max m_i,  l = sum_i 2^(m_i - M) l_i,  O = sum_i 2^(m_i - M) O_i.
 //
-// What bounds it: a step reads every cached K and V row once and does 4 d flops per row
-// and key with it, G * q_len (4 to 16) flops a byte, far under the tensor cores' 250; so
-// it is the cache's bytes over the memory bandwidth.  The kernel is built to keep TMA
-// loads in flight and to give every SM the same number of bytes:
+// What bounds it: up to 16 rows (G * q_len) per kv-head a step reads every cached K and V row
+// once and does 4 d flops per row and key with it, one a byte and row in BF16 and two in FP8, far
+// under the tensor cores' 250; so it is the cache's bytes over the memory bandwidth.  More rows
+// are more units, and each reads K and V again (figures below).  The kernel is built to keep
+// TMA loads in flight and to give every SM the same number of bytes:
 //   - The work is a line of 64-token tiles (one K page and one V page of one kv-head),
 //     sequence after sequence; every CTA of one resident round takes an equal share, the
 //     lengths being read on the device.  A unit (the up to 16 rows that read one kv-head
@@ -32,9 +33,11 @@
 //     of V, which the matrix instruction wants in both; it has float32's range.
 //     The sums l are those of the unrounded p.
 // Measured on one B200, whole calls: four ragged BF16 sequences of up to 128K tokens, 32 q- and
-// 8 kv-heads of 128, 216 to 220 us (all of the copy rate); 48 of up to 4K with four new tokens
-// each, 78 us (80 %: the start, and 1 us to join the warps of a unit); one FP8 sequence of 128K,
-// 53 us (77 %: twelve consumer warps of 128 registers an SM and their chains of dependent steps;
+// 8 kv-heads of 128, 214 to 219 us (all of the copy rate); 48 of up to 4K with four new tokens
+// each, 78 us (80 %: the start, and 1 us to join the warps of a unit); four of 128K with 4 / 16 /
+// 20 / 32 / 64 rows per kv-head, BF16 314 / 327 / 635 / 631 / 1232 us (a reading's bytes at the copy
+// rate: 328), FP8 195 / 191 / 387 / 370 / 763 to 810 (164); one FP8 sequence of 128K,
+// 52 to 54 us (77 %: twelve consumer warps of 128 registers an SM and their chains of dependent steps;
 // the scheduler issues in 45 % of the cycles, the ALU with the 64 conversions per warp and
 // tile is 44 % busy, the matrix pipe 37 %.  The e4m3 form of the product for S: 55.7.  V's codes
 // shifted into place instead of converted: 55.9, and 59 to 63 with the test for NaN codes that

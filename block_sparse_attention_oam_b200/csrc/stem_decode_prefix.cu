@@ -2,12 +2,13 @@
 //
 // All sequences of the batch see the same prefix, so a kv-head's rows are all of the batch's:
 // B * q_len * G of them (256 for 64 sequences of Qwen3-8B's layer), over K and V that are read
-// once.  Here the work is a product of that many rows, 4 d flops per row and key against
-// 4 d bytes per key: 64 rows a byte, up to what the tensor cores need (250 flops a byte).
+// once per pair of row tiles.  Here the work is a product of that many rows, 4 d flops per row
+// and key against 4 d bytes per key in BF16 (2 d in FP8): one flop a byte and row (two), so that
+// the 256 rows of a pair make 256 (512), about what the tensor cores need (250).
 //
 // One CTA per SM, on two thirds of them; decode_kernel reads the own tokens on the others
-// meanwhile, since this kernel is bound by what goes on inside an SM.  Work unit: one kv-head and two row tiles ("slots") of floor(128 / G)
-// tokens each, G rows per token; the unit's keys, in tiles of 128 (two pages), are split
+// meanwhile (kPrefixCtas has the figures).  Work unit: one kv-head and two row tiles ("slots")
+// of floor(128 / G) tokens each, G rows per token; the unit's keys, in tiles of 128 (two pages), are split
 // evenly over the CTAs as in decode_kernel (a line, gangs of CTAs on neighbouring heads), and
 // each CTA leaves its share's (m, l, O) for decode_finish.
 //   warp 0      TMA producer: the unit's Q tiles, then K and V tiles through shared rings
@@ -20,11 +21,14 @@
 //   warps 18,19 (FP8) widen V's codes to f16 in shared memory: with P in f16 the product
 //               carries P to 2^-11, where an e4m3 P would lose 2^-4 of every weight; S stays
 //               an e4m3 product, which is exact
-// A tile of 256 rows takes 3.8 thousand cycles, its products and its exponentials 2.0 thousand
-// each: with S and O of two slots the 512 TMEM columns are full, so a slot's S waits for its
-// last product.  Tiles of 64 keys with a second S took 95 us where these took 85.
+// A 128-key tile of 256 rows takes 2.06 us in BF16 and 1.98 in FP8 (calls of 64 sequences behind
+// 32K to 128K tokens, by the difference; 4.06 thousand cycles at 1965 MHz), in which the matrix
+// pipe is active 70 % and XU (exponentials, the packing of P) 72 %: with S and O of two slots
+// the 512 TMEM columns are full, so a slot's S waits for its last product.  Tiles of 64 keys with a
+// second S took 95 us where these took 85.
 // Measured on one B200, whole calls, 32 q- and 8 kv-heads of 128: 64 sequences of up to 1K own
-// tokens behind 32768 shared ones, BF16, 73 to 80 us; 128 of up to 512 behind 16384, FP8, 72 us.
+// tokens behind 32768 shared ones, BF16, 72 to 81 us, of which 44 are the tiles and 8 the joining
+// after the last of them; 128 of up to 512 behind 16384, FP8, 71 to 73 us.
 // P in f16 is taken as 2^(s - m + 7), as in decode_kernel, so that a long tail of small weights
 // counts; BF16 rounds P to bf16, as V is.  V rows behind the prefix's end (the rest of its last page)
 // are set to zero in shared memory, since they may hold NaN and 0 * NaN is not 0.

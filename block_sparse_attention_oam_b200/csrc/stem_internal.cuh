@@ -495,9 +495,14 @@ inline int gang_of(int Hkv) {
 // of (kv-head, pair of row tiles), each `tiles` 128-key tiles and kPrefixUnitCost empty ones
 // long on a gang member's line, of which every CTA takes `per`.
 // An SM each, first in the step's stream; decode_kernel runs beside them on the others, for
-// whose loads these products leave the memory free.  64 sequences with 512 tokens behind 32768
-// shared ones: 82 us one kernel after the other on all 148 SMs, 72 with 96 CTAs here (68 with
-// 104, which 256 sequences of 64 tokens behind 8192 shared ones pay: 73 and 79).
+// whose loads these products leave the memory free.  us a call with 96 / 104 / 120 / 148 CTAs here:
+//   64 sequences behind 32768 shared tokens, own tokens 64   70 / 66 / 62 / 62
+//                                                       512   72 / 68 / 77 / 82
+//                                                      1024   87 / 94 / 94 / 101
+//                                                      4096  199 / 201 / 206 / 217
+//   256 sequences of 64 behind 8192                           76 / 79 / 110 / 86
+//   128 sequences of 512 behind 16384, FP8                    90 / 100 / 94 / 93
+// 96 gives up a tenth where own tokens are few, 6 % at 512, and is ahead of all others elsewhere.
 constexpr int kPrefixCtas = 96;
 constexpr int kPrefixTile = 128;
 constexpr int kPrefixUnitCost = 2;

@@ -291,7 +291,10 @@ typedef struct {
   int collect_weights;         /* 1: also add up the softmax weights each cached token receives */
 } stem_decode_t;
 
-/* Device workspace bytes of stem_decode (0 on a bad problem).  Host only. */
+/* Device workspace bytes of stem_decode (0 on a bad problem).  Host only.  collect_weights adds
+ * the scores of every row and possible token: num_seqs x q_len x num_q_heads x max_kv_len (rounded
+ * up to whole pages) x 4 bytes, however short the sequences are (64 sequences of at most 128K with
+ * 32 heads: 1.07 GB). */
 STEM_API size_t stem_decode_workspace_size(const stem_decode_t* dec);
 
 /*
@@ -308,8 +311,13 @@ STEM_API size_t stem_decode_workspace_size(const stem_decode_t* dec);
  *   value outside is clamped and reported as STEM_ERR_BOUNDS, as is a page outside the
  *   cache, which is read as slot 0.
  * prefix_table: DEVICE int32 [ceil(prefix_len / 64)] slots of the prefix in the same
- *   cache, or NULL with prefix_len 0.  The prefix is read once for the whole batch, and
+ *   cache, or NULL with prefix_len 0.  The prefix is held once for the whole batch, and
  *   kv_lens count only the tokens behind it.
+ * What is read of the cache: a sequence's own K and V once per 16 of its rows of a kv-head, of
+ *   which it has q_len x Hq / Hkv (once for up to 16, twice for 17 to 32, ...).  The prefix's
+ *   once per 16 of the whole batch's rows of a kv-head where these are 32 at most or
+ *   Hq / Hkv > 128; else once per 2 floor(128 / (Hq / Hkv)) tokens of the batch (256 rows where
+ *   Hq / Hkv divides 128).
  * weights_in, weights_out (collect_weights 1): DEVICE float [B, Hkv, weights_stride],
  *   weights_stride >= max_kv_len:
  *     weights_out[b, kh, j] = weights_in[b, kh, j] + sum of token j's softmax weight over
